@@ -57,6 +57,12 @@ class Fp8Weights(ctypes.Structure):
                  "bias")]
 
 
+class Fp8BlockWeights(ctypes.Structure):
+    """fp4moe_fp8_block_weights"""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("w13", "w13_scale", "w2", "w2_scale", "sh13", "sh13_scale", "sh2", "sh2_scale")]
+
+
 class WsLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("status", "logits", "topk_idx", "topk_w", "expert_count", "expert_slot", "route_row",
@@ -118,13 +124,22 @@ def lib() -> ctypes.CDLL:
         L.fp4moe_route_noalloc_scratch_bytes.argtypes = [P(Dims)]
         L.fp4moe_route_noalloc_scratch_bytes.restype = sz
         L.fp4moe_route_noalloc_status.argtypes = [vp, P(i32), P(i64)]
+        L.fp4moe_add_rmsnorm_fp8.argtypes = [vp, i64, vp, vp, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]
+        L.fp4moe_swiglu_fp8.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+        L.fp4moe_linear_fp8_block_workspace_size.argtypes = [i32, i32, i32]
+        L.fp4moe_linear_fp8_block_workspace_size.restype = sz
+        L.fp4moe_linear_fp8_block.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i64, i32, vp, sz, vp]
+        L.fp4moe_experts_fp8_block_workspace_size.argtypes = [P(Dims)]
+        L.fp4moe_experts_fp8_block_workspace_size.restype = sz
+        L.fp4moe_experts_fp8_block.argtypes = [P(Dims), P(Fp8BlockWeights), vp, vp, vp, vp, vp, vp, sz, vp]
         for name in ("fp4moe_workspace_layout", "fp4moe_pack_scales", "fp4moe_pack_weights", "fp4moe_pack_gateup_weights",
                      "fp4moe_pack_gateup_scales", "fp4moe_route", "fp4moe_quantize_act",
                      "fp4moe_forward", "fp4moe_forward_cols", "fp4moe_forward_w8a8", "fp4moe_forward_nvfp4_emulated", "fp4moe_linear",
                      "fp4moe_mxfp4_to_fp8_rowscale",
                      "fp4moe_clear_status",
                      "fp4moe_get_status", "fp4moe_route_noalloc", "fp4moe_route_noalloc_status",
-                     "fp4moe_check_scales"):
+                     "fp4moe_check_scales", "fp4moe_add_rmsnorm_fp8", "fp4moe_swiglu_fp8", "fp4moe_linear_fp8_block",
+                     "fp4moe_experts_fp8_block"):
             getattr(L, name).restype = i32
         _LIB = L
     return _LIB
@@ -250,6 +265,43 @@ def mxfp4_to_fp8_rowscale(codes: int, scales: int, rows: int, K: int, fp8_out: i
                           row_status: int | None, ws: int, ws_bytes: int, stream: int = 0) -> None:
     _ok(lib().fp4moe_mxfp4_to_fp8_rowscale(codes, scales, rows, K, fp8_out, row_scale, row_status, ws, ws_bytes,
                                            stream), "fp4moe_mxfp4_to_fp8_rowscale")
+
+
+def add_rmsnorm_fp8(x: int, x_ld: int, residual: int | None, gamma: int, T: int, H: int, eps: float,
+                    residual_out: int | None, y: int | None, q: int | None, scales: int | None,
+                    stream: int = 0) -> None:
+    _ok(lib().fp4moe_add_rmsnorm_fp8(x, x_ld, residual, gamma, T, H, eps, residual_out, y, q, scales, stream),
+        "fp4moe_add_rmsnorm_fp8")
+
+
+def swiglu_fp8(gu: int, gu_ld: int, T: int, I: int, q: int, scales: int, stream: int = 0) -> None:
+    _ok(lib().fp4moe_swiglu_fp8(gu, gu_ld, T, I, q, scales, stream), "fp4moe_swiglu_fp8")
+
+
+def linear_fp8_block_workspace_size(T: int, K: int, N: int) -> int:
+    n = lib().fp4moe_linear_fp8_block_workspace_size(T, K, N)
+    if n == 0:
+        raise Fp4MoeError(2, "fp4moe_linear_fp8_block_workspace_size")
+    return n
+
+
+def linear_fp8_block(T: int, K: int, N: int, xq: int, xs: int, w: int, w_scale: int, out: int, out_ld: int,
+                     out_is_fp32: bool, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    _ok(lib().fp4moe_linear_fp8_block(T, K, N, xq, xs, w, w_scale, out, out_ld, int(out_is_fp32), ws, ws_bytes,
+                                      stream), "fp4moe_linear_fp8_block")
+
+
+def experts_fp8_block_workspace_size(dims: Dims) -> int:
+    n = lib().fp4moe_experts_fp8_block_workspace_size(ctypes.byref(dims))
+    if n == 0:
+        raise Fp4MoeError(2, "fp4moe_experts_fp8_block_workspace_size")
+    return n
+
+
+def experts_fp8_block(dims: Dims, weights: Fp8BlockWeights, xq: int, xs: int, topk_idx: int, topk_w: int, out: int,
+                      ws: int, ws_bytes: int, stream: int = 0) -> None:
+    _ok(lib().fp4moe_experts_fp8_block(ctypes.byref(dims), ctypes.byref(weights), xq, xs, topk_idx, topk_w, out, ws,
+                                       ws_bytes, stream), "fp4moe_experts_fp8_block")
 
 
 def check_scales(scales: int, n: int, fmt: int, ws: int, ws_bytes: int, stream: int = 0) -> None:

@@ -1,0 +1,238 @@
+// Block-scaled FP8 activations: residual addition + RMS norm, and SwiGLU,
+// each with E4M3 codes and one fp32 scale per 128 columns.
+//
+// Both read their inputs once and write their outputs once (HBM bound): a
+// thread holds 8 consecutive columns (one 16-byte bf16 load), 16 lanes one
+// scale block, whose largest magnitude is a 16-lane shuffle reduction.
+#include "fp8_block.cuh"
+#include "internal.h"
+
+namespace fp4moe {
+
+namespace {
+
+struct NormParams {
+  const uint16_t *x, *residual, *gamma;
+  uint16_t *residual_out, *y;
+  uint8_t* q;
+  float* scales;
+  int64_t x_ld;
+  int H;
+  float eps;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* v) {
+  v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+  v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+}
+
+// Codes and scale of the 16-lane group's block from each lane's 8 values; all
+// 32 lanes take part (v = 0 past the row's end).
+__device__ __forceinline__ void quant_block(const float* v, bool in, uint8_t* q, float* scale) {
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[j]));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float s = e4m3_scale(amax);
+  if (in) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3], s), e4m3x4(v[4], v[5], v[6], v[7], s));
+    if ((threadIdx.x & 15) == 0) *scale = s;
+  }
+}
+
+// One CTA per row; CH 8-column chunks per thread, kept in registers between
+// the sum of squares and the output.
+template <int CH>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams p) {
+  __shared__ float part[32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = blockIdx.x;
+  const int chunks = p.H >> 3;
+  float v[CH][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (c < chunks) {
+      unpack8(*reinterpret_cast<const uint4*>(p.x + row * p.x_ld + 8 * c), v[i]);
+      if (p.residual) {
+        float r[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.residual + row * p.H + 8 * c), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+      }
+      if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + row * p.H + 8 * c) = pack8(v[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  ss = 0.f;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) ss += part[w];
+  const float r = rsqrtf(__fdiv_rn(ss, (float)p.H) + p.eps);
+  const int nb = blocks128(p.H);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+    const bool in = c < chunks;
+    if (in) {
+      float g[8];
+      unpack8(*reinterpret_cast<const uint4*>(p.gamma + 8 * c), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
+      if (p.y) *reinterpret_cast<uint4*>(p.y + row * p.H + 8 * c) = pack8(v[i]);
+    }
+    if (p.q) quant_block(v[i], in, p.q + row * p.H + 8 * c, p.scales + row * nb + (c >> 4));
+  }
+}
+
+// Thread per 8 columns of h; rows padded to whole scale blocks so that a
+// 16-lane group never spans two rows.
+__global__ void __launch_bounds__(256) swiglu_fp8_kernel(const uint16_t* gu, int64_t gu_ld, int64_t T, int I,
+                                                         uint8_t* q, float* scales) {
+  pdl_wait();
+  pdl_trigger();
+  const int nb = blocks128(I), per_row = nb * 16;
+  const int64_t n = T * per_row;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t row = i / per_row;
+  const int c = (int)(i - row * per_row);
+  const bool in = i < n && 8 * c < I;
+  float h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = 0.f;
+  if (in) {
+    float g[8], u[8];
+    const uint16_t* src = gu + row * gu_ld + 8 * c;
+    unpack8(*reinterpret_cast<const uint4*>(src), g);
+    unpack8(*reinterpret_cast<const uint4*>(src + I), u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = swiglu(g[j], u[j]);
+  }
+  quant_block(h, in, q + row * I + 8 * c, scales + row * nb + (c >> 4));
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const uint16_t* x, int64_t x_ld, const uint16_t* residual, const uint16_t* gamma, int T,
+                               int H, float eps, uint16_t* residual_out, uint16_t* y, uint8_t* q, float* scales,
+                               cudaStream_t s) {
+  const NormParams p{x, residual, gamma, residual_out, y, q, scales, x_ld, H, eps};
+  const int chunks = H / 8;
+  int ch = 1;
+  while (ch < 8 && chunks > 512 * ch) ch *= 2;
+  const dim3 block((unsigned)(((chunks + ch - 1) / ch + 31) / 32 * 32));
+  switch (ch) {
+    case 1: return launch_pdl(add_rmsnorm_kernel<1>, dim3(T), block, 0, s, p);
+    case 2: return launch_pdl(add_rmsnorm_kernel<2>, dim3(T), block, 0, s, p);
+    case 4: return launch_pdl(add_rmsnorm_kernel<4>, dim3(T), block, 0, s, p);
+    default: return launch_pdl(add_rmsnorm_kernel<8>, dim3(T), block, 0, s, p);
+  }
+}
+
+cudaError_t launch_swiglu_fp8(const uint16_t* gu, int64_t gu_ld, int T, int I, uint8_t* q, float* scales,
+                              cudaStream_t s) {
+  const int64_t n = (int64_t)T * blocks128(I) * 16;
+  return launch_pdl(swiglu_fp8_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, gu, gu_ld, (int64_t)T, I, q,
+                    scales);
+}
+
+}  // namespace fp4moe
+
+using namespace fp4moe;
+
+namespace {
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+constexpr int32_t kMaxRows = 1 << 20;  // rows of one call
+constexpr int32_t kMaxCols = 65536;
+}  // namespace
+
+extern "C" {
+
+fp4moe_status fp4moe_add_rmsnorm_fp8(const uint16_t* x, int64_t x_ld, const uint16_t* residual, const uint16_t* gamma,
+                                     int32_t T, int32_t H, float eps, uint16_t* residual_out, uint16_t* y, uint8_t* q,
+                                     float* scales, void* stream) {
+  if (!x || !gamma || (!y && !q) || (q != nullptr) != (scales != nullptr)) return FP4MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxRows || H < 16 || H > kMaxCols || H % 16 != 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
+  if (x_ld < H || x_ld % 8 != 0 || !(eps >= 0.f)) return FP4MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(residual_out, 16) ||
+      !aligned(y, 16) || !aligned(q, 16) || !aligned(scales, 4))
+    return FP4MOE_ERR_INVALID_ARG;
+  if (T == 0) return FP4MOE_OK;
+  if (fp4moe_status st = check_device()) return st;
+  return cuda_status(
+      launch_add_rmsnorm(x, x_ld, residual, gamma, T, H, eps, residual_out, y, q, scales, static_cast<cudaStream_t>(stream)));
+}
+
+fp4moe_status fp4moe_swiglu_fp8(const uint16_t* gu, int64_t gu_ld, int32_t T, int32_t I, uint8_t* q, float* scales,
+                                void* stream) {
+  if (!gu || !q || !scales) return FP4MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxRows || I < 16 || I > kMaxCols || I % 16 != 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
+  if (gu_ld < 2 * (int64_t)I || gu_ld % 8 != 0) return FP4MOE_ERR_INVALID_ARG;
+  if (!aligned(gu, 16) || !aligned(q, 16) || !aligned(scales, 4)) return FP4MOE_ERR_INVALID_ARG;
+  if (T == 0) return FP4MOE_OK;
+  if (fp4moe_status st = check_device()) return st;
+  return cuda_status(launch_swiglu_fp8(gu, gu_ld, T, I, q, scales, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp4moe_linear_fp8_block_workspace_size(int32_t T, int32_t K, int32_t N) {
+  if (T < 0 || T > kMaxRows || K < 16 || K > kMaxCols || K % 16 != 0 || N < 1 || N > kMaxRows) return 0;
+  return linear_fp8_workspace(T, K, N);
+}
+
+fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uint8_t* xq, const float* xs,
+                                      const uint8_t* w, const float* w_scale, void* out, int64_t out_ld,
+                                      int32_t out_is_fp32, void* ws, size_t ws_bytes, void* stream) {
+  if (!xq || !xs || !w || !w_scale || !out || !ws) return FP4MOE_ERR_INVALID_ARG;
+  const size_t need = fp4moe_linear_fp8_block_workspace_size(T, K, N);
+  if (need == 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < need) return FP4MOE_ERR_WORKSPACE;
+  if (out_ld < N || !aligned(xq, 16) || !aligned(w, 16) || !aligned(xs, 4) || !aligned(w_scale, 4) ||
+      !aligned(out, out_is_fp32 ? 4 : 2) || !aligned(ws, 16))
+    return FP4MOE_ERR_INVALID_ARG;
+  if (T == 0) return FP4MOE_OK;
+  if (fp4moe_status st = check_device()) return st;
+  const LinearFp8Args a{T, K, N, xq, xs, w, w_scale, out, out_ld, out_is_fp32 != 0, ws};
+  return cuda_status(launch_linear_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp4moe_experts_fp8_block_workspace_size(const fp4moe_dims* dims) {
+  Layout L;
+  if (!dims || dims->fmt != FP4MOE_FP8 || dims->T > kExpertsMaxT || !make_layout(*dims, &L)) return 0;
+  return experts_fp8_workspace(*dims);
+}
+
+fp4moe_status fp4moe_experts_fp8_block(const fp4moe_dims* dims, const fp4moe_fp8_block_weights* w, const uint8_t* xq,
+                                       const float* xs, const int32_t* topk_idx, const float* topk_w, uint16_t* out,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  if (!dims || !w || !xq || !xs || !topk_idx || !topk_w || !out || !ws) return FP4MOE_ERR_INVALID_ARG;
+  if (dims->fmt != FP4MOE_FP8) return FP4MOE_ERR_INVALID_ARG;
+  const size_t need = fp4moe_experts_fp8_block_workspace_size(dims);
+  if (need == 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < need) return FP4MOE_ERR_WORKSPACE;
+  if (!w->w13 || !w->w13_scale || !w->w2 || !w->w2_scale) return FP4MOE_ERR_INVALID_ARG;
+  if (dims->n_shared && (!w->sh13 || !w->sh13_scale || !w->sh2 || !w->sh2_scale)) return FP4MOE_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)xq, (const void*)w->w13, (const void*)w->w2, (const void*)w->sh13,
+                        (const void*)w->sh2, (const void*)out, (const void*)ws})
+    if (!aligned(q, 16)) return FP4MOE_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)xs, (const void*)w->w13_scale, (const void*)w->w2_scale,
+                        (const void*)w->sh13_scale, (const void*)w->sh2_scale, (const void*)topk_idx,
+                        (const void*)topk_w})
+    if (!aligned(q, 4)) return FP4MOE_ERR_INVALID_ARG;
+  if (fp4moe_status st = check_device()) return st;
+  return cuda_status(
+      launch_experts_fp8(*dims, *w, xq, xs, topk_idx, topk_w, out, ws, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -134,6 +134,33 @@ cudaError_t launch_pack_scales(const uint8_t* src, uint8_t* dst, int64_t n_mat, 
 cudaError_t launch_convert(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, uint8_t* out,
                            float* row_scale, uint8_t* row_status, int32_t* status, cudaStream_t s);
 
+// ------------------------------------------------------------- block-scaled FP8
+// E4M3 with one fp32 scale per 128 columns (activations) or 128 x 128 block
+// (weights); csrc/fp8_block.cu holds the entry points' checks.
+cudaError_t launch_add_rmsnorm(const uint16_t* x, int64_t x_ld, const uint16_t* residual, const uint16_t* gamma, int T,
+                               int H, float eps, uint16_t* residual_out, uint16_t* y, uint8_t* q, float* scales,
+                               cudaStream_t s);
+cudaError_t launch_swiglu_fp8(const uint16_t* gu, int64_t gu_ld, int T, int I, uint8_t* q, float* scales,
+                              cudaStream_t s);
+struct LinearFp8Args {
+  int T, K, N;
+  const uint8_t* xq;
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  void* out;
+  int64_t out_ld;
+  bool out_fp32;
+  void* scratch;
+};
+size_t linear_fp8_workspace(int T, int K, int N);
+cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
+constexpr int kExpertsMaxT = 16;
+size_t experts_fp8_workspace(const fp4moe_dims& d);
+cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weights& w, const uint8_t* xq,
+                               const float* xs, const int32_t* topk_idx, const float* topk_w, uint16_t* out, void* ws,
+                               cudaStream_t s);
+
 // ------------------------------------------------------------- grouped GEMMs
 struct GemmArgs {
   const fp4moe_dims* d;

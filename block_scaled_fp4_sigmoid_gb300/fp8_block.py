@@ -1,0 +1,211 @@
+"""Block-scaled FP8 operators on tensors: E4M3 codes with one fp32 scale per
+token and 128 columns (activations) or per 128 x 128 block (weights).
+
+The functions check their tensors, allocate what the caller does not pass and
+call the library on the current stream of the tensors' device.  Codes are
+torch.uint8 or torch.float8_e4m3fn tensors.  ``Fp8BlockMlp`` and
+``Fp8BlockMoE`` run them together as the two feed-forward sublayers of a
+decoder layer.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (FP8, Dims, Fp8BlockWeights, add_rmsnorm_fp8 as _add_rmsnorm, experts_fp8_block as _experts,
+               experts_fp8_block_workspace_size, linear_fp8_block as _linear, linear_fp8_block_workspace_size,
+               make_dims, route as _route, swiglu_fp8 as _swiglu, workspace_size)
+
+BLOCK = 128
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _check(name, t, shape, dtypes, device, dense=True):
+    """A tensor of the given shape, one of the types and the device; dense (row-major)
+    or, for a matrix, with unit stride along its rows."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device:
+        raise ValueError(f"{name}: expected {shape} of {dtypes} on {device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+    if not (t.is_contiguous() if dense else t.stride(1) == 1 or t.shape[1] <= 1):
+        raise ValueError(f"{name}: {'row-major' if dense else 'unit column stride'} expected, strides are {t.stride()}")
+
+
+def _ld(t):
+    """Row stride of a matrix in elements (one row: its length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _out(name, t, shape, dtypes, device, dense=True):
+    if t is None:
+        return torch.empty(shape, dtype=dtypes[0], device=device)
+    _check(name, t, shape, dtypes, device, dense)
+    return t
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None, q=None, scales=None,
+                    want_y: bool = False):
+    """z = x + residual, v = z rsqrt(mean(z^2) + eps) gamma; returns (bf16(z), bf16(v), codes of
+    v, scales) (fp4moe_add_rmsnorm_fp8).  x bf16 [T, H], rows may be strided; residual bf16
+    [T, H] or None (then bf16(z) is x itself).  bf16(v) is written when y is passed or
+    want_y is set, else None is returned in its place."""
+    if x.dim() != 2:
+        raise ValueError(f"x: a matrix expected, got {tuple(x.shape)}")
+    T, H = x.shape
+    dev = x.device
+    _check("x", x, (T, H), _BF16, dev, dense=False)
+    _check("gamma", gamma, (H,), _BF16, dev)
+    if residual is not None:
+        _check("residual", residual, (T, H), _BF16, dev)
+        residual_out = _out("residual_out", residual_out, (T, H), _BF16, dev)
+    elif residual_out is not None:
+        _check("residual_out", residual_out, (T, H), _BF16, dev)
+    if y is not None or want_y:
+        y = _out("y", y, (T, H), _BF16, dev)
+    q = _out("q", q, (T, H), _CODES, dev)
+    scales = _out("scales", scales, (T, _blocks(H)), _F32, dev)
+    if T:
+        _add_rmsnorm(x.data_ptr(), _ld(x), _ptr(residual), gamma.data_ptr(), T, H, eps, _ptr(residual_out), _ptr(y),
+                     q.data_ptr(), scales.data_ptr(), _stream(dev))
+    return residual_out if residual_out is not None else x, y, q, scales
+
+
+def swiglu_fp8(gu, *, q=None, scales=None):
+    """(codes, scales) of silu(gu[:, :I]) * gu[:, I:] (fp4moe_swiglu_fp8); gu bf16 [T, 2I], rows
+    may be strided."""
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError(f"gu: [T, 2I] expected, got {tuple(gu.shape)}")
+    T, I = gu.shape[0], gu.shape[1] // 2
+    dev = gu.device
+    _check("gu", gu, (T, 2 * I), _BF16, dev, dense=False)
+    q = _out("q", q, (T, I), _CODES, dev)
+    scales = _out("scales", scales, (T, _blocks(I)), _F32, dev)
+    if T:
+        _swiglu(gu.data_ptr(), _ld(gu), T, I, q.data_ptr(), scales.data_ptr(), _stream(dev))
+    return q, scales
+
+
+def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, ws=None):
+    """out [T, N] = x . W^T for codes xq [T, K] with scales xs [T, K/128] and w [N, K] with
+    w_scale [N/128, K/128] (fp4moe_linear_fp8_block; blocks rounded up).  out: bf16 or fp32,
+    rows may be strided.  ws: a uint8 tensor of linear_fp8_block_workspace_size(T, K, N) bytes,
+    or None (allocated here); its status word is read by get_status."""
+    if xq.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"xq and w: matrices expected, got {tuple(xq.shape)} and {tuple(w.shape)}")
+    (T, K), N = xq.shape, w.shape[0]
+    dev = xq.device
+    _check("xq", xq, (T, K), _CODES, dev)
+    _check("xs", xs, (T, _blocks(K)), _F32, dev)
+    _check("w", w, (N, K), _CODES, dev)
+    _check("w_scale", w_scale, (_blocks(N), _blocks(K)), _F32, dev)
+    out = _out("out", out, (T, N), (out_dtype,) if out is None else _BF16 + _F32, dev, dense=False)
+    if out.dtype not in _BF16 + _F32:
+        raise ValueError(f"out: bf16 or fp32, got {out.dtype}")
+    if T:
+        n = linear_fp8_block_workspace_size(T, K, N)
+        if ws is None:
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), _ld(out),
+                out.dtype == torch.float32, ws.data_ptr(), ws.numel(), _stream(dev))
+    return out
+
+
+def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh13=None, sh13_scale=None, sh2=None,
+                      sh2_scale=None, *, out=None, ws=None):
+    """bf16 [T, H]: the routed experts of up to 16 tokens, plus the shared one where given
+    (fp4moe_experts_fp8_block).  xq [T, H], xs [T, H/128]; topk_idx int32 and topk_w fp32 [T, k]
+    (an index outside [0, E) is skipped); w13 [E, 2I, H], w2 [E, H, I] with one scale per 128 x
+    128 block."""
+    if xq.dim() != 2 or topk_idx.dim() != 2 or w13.dim() != 3:
+        raise ValueError(f"xq, topk_idx, w13: two, two and three dimensions expected, got {tuple(xq.shape)}, "
+                         f"{tuple(topk_idx.shape)}, {tuple(w13.shape)}")
+    (T, H), k, E, I = xq.shape, topk_idx.shape[1], w13.shape[0], w13.shape[1] // 2
+    dev = xq.device
+    _check("xq", xq, (T, H), _CODES, dev)
+    _check("xs", xs, (T, _blocks(H)), _F32, dev)
+    _check("topk_idx", topk_idx, (T, k), (torch.int32,), dev)
+    _check("topk_w", topk_w, (T, k), _F32, dev)
+    hb, ib = _blocks(H), _blocks(I)
+    _check("w13", w13, (E, 2 * I, H), _CODES, dev)
+    _check("w13_scale", w13_scale, (E, 2 * ib, hb), _F32, dev)
+    _check("w2", w2, (E, H, I), _CODES, dev)
+    _check("w2_scale", w2_scale, (E, hb, ib), _F32, dev)
+    if sh13 is not None:
+        _check("sh13", sh13, (2 * I, H), _CODES, dev)
+        _check("sh13_scale", sh13_scale, (2 * ib, hb), _F32, dev)
+        _check("sh2", sh2, (H, I), _CODES, dev)
+        _check("sh2_scale", sh2_scale, (hb, ib), _F32, dev)
+    dims = make_dims(T, H, I, E, k, n_shared=int(sh13 is not None), fmt=FP8)
+    n = experts_fp8_block_workspace_size(dims)
+    out = _out("out", out, (T, H), _BF16, dev)
+    if ws is None:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    weights = Fp8BlockWeights(w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), _ptr(sh13),
+                              _ptr(sh13_scale), _ptr(sh2), _ptr(sh2_scale))
+    _experts(dims, weights, xq.data_ptr(), xs.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(),
+             ws.data_ptr(), ws.numel(), _stream(dev))
+    return out
+
+
+class Fp8BlockMlp:
+    """A dense feed-forward sublayer: norm -> gate/up product -> SwiGLU -> down
+    product, on block-scaled FP8 weights w13 [2I, H] (gate rows, then up rows)
+    and w2 [H, I]."""
+
+    def __init__(self, gamma, w13, w13_scale, w2, w2_scale, eps: float = 1e-6):
+        self.gamma, self.eps = gamma, eps
+        self.w13, self.w13_scale, self.w2, self.w2_scale = w13, w13_scale, w2, w2_scale
+
+    def forward(self, x, residual=None):
+        """(output bf16 [T, H], residual stream bf16 [T, H]) for x bf16 [T, H]: the caller adds
+        the output to the residual stream in its next norm."""
+        res, _, q, s = add_rmsnorm_fp8(x, residual, self.gamma, self.eps)
+        gu = linear_fp8_block(q, s, self.w13, self.w13_scale)
+        hq, hs = swiglu_fp8(gu)
+        return linear_fp8_block(hq, hs, self.w2, self.w2_scale), res
+
+
+class Fp8BlockMoE:
+    """A mixture-of-experts feed-forward sublayer for up to 16 tokens: norm ->
+    router (fp4moe_route on the bf16 norm output) -> experts (and the shared
+    one) on block-scaled FP8 weights.  dims: as make_dims returns for the
+    layer with fmt=FP8; w_router bf16 [E, H], bias fp32 [E]."""
+
+    def __init__(self, dims: Dims, gamma, w_router, bias, w13, w13_scale, w2, w2_scale, sh13=None, sh13_scale=None,
+                 sh2=None, sh2_scale=None, eps: float = 1e-6):
+        if dims.fmt != FP8 or dims.n_shared != int(sh13 is not None):
+            raise ValueError("dims: fmt FP8, and n_shared as the shared expert's weights say")
+        self.dims, self.gamma, self.w_router, self.bias, self.eps = dims, gamma, w_router, bias, eps
+        self.weights = (w13, w13_scale, w2, w2_scale, sh13, sh13_scale, sh2, sh2_scale)
+        self.device = w13.device
+        _check("w_router", w_router, (dims.E, dims.H), _BF16, self.device)
+        _check("bias", bias, (dims.E,), _F32, self.device)
+        self.ws_bytes = workspace_size(dims)  # of the router
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.experts_ws = torch.empty(experts_fp8_block_workspace_size(dims), dtype=torch.uint8, device=self.device)
+
+    def route(self, y):
+        """(topk_idx, topk_w) of the bf16 rows y [T, H]."""
+        d = self.dims
+        _check("y", y, (d.T, d.H), _BF16, self.device)
+        idx = torch.empty((d.T, d.top_k), dtype=torch.int32, device=self.device)
+        w = torch.empty((d.T, d.top_k), dtype=torch.float32, device=self.device)
+        _route(d, y.data_ptr(), self.w_router.data_ptr(), self.bias.data_ptr(), idx.data_ptr(), w.data_ptr(), None,
+               self.ws.data_ptr(), self.ws_bytes, _stream(self.device))
+        return idx, w
+
+    def forward(self, x, residual=None):
+        """As Fp8BlockMlp.forward."""
+        res, y, q, s = add_rmsnorm_fp8(x, residual, self.gamma, self.eps, want_y=True)
+        idx, w = self.route(y)
+        return experts_fp8_block(q, s, idx, w, *self.weights, ws=self.experts_ws), res

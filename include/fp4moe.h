@@ -423,6 +423,88 @@ fp4moe_status fp4moe_linear(int32_t fmt, int32_t T, int32_t K, int32_t N, const 
                             const uint8_t *w_scale, const float *g_w, uint16_t *out, void *ws, size_t ws_bytes,
                             void *stream);
 
+/* ---- Block-scaled FP8: the E4M3 side of the same decoder layer --------------
+ * Activations: E4M3 codes q [T, n] row-major with fp32 scales [T, nb],
+ * nb = ceil(n / 128), one per token and 128 columns; the value of column c is
+ * q[t, c] * scale[t, c / 128].  Weights: E4M3 codes [N, K] row-major with fp32
+ * scales [ceil(N / 128), ceil(K / 128)], one per 128 x 128 block (the last
+ * blocks may be partial).  The quantising calls use scale = fp32(amax / 448)
+ * and code = RNE_E4M3(fp32(v / scale)); a block of zeros has scale 0 and
+ * signed zeros; a NaN in a block makes its scale NaN.
+ * Every sum, norm and scale product is held in fp32. */
+
+/* Residual addition, RMS norm and E4M3 quantisation in one pass over a row:
+ *   z = x + residual (fp32; residual nullable: z = x)
+ *   residual_out = bf16(z)                                    (nullable)
+ *   v = z * rsqrt(mean(z^2) + eps) * gamma
+ *   y = bf16(v)                                                (nullable)
+ *   q [T, H], scales [T, ceil(H / 128)] = the codes of v      (nullable, both or neither)
+ * At least one of y and q is asked for.  x bf16 [T, H] with row stride x_ld
+ * elements (>= H, a multiple of 8); residual, residual_out, y bf16 [T, H];
+ * gamma bf16 [H].  residual_out may be x (with x_ld = H) or residual.
+ * 0 <= T <= 2^20 (T = 0: nothing is done), 16 <= H <= 65536, H % 16 == 0;
+ * eps >= 0; pointers 16-byte aligned (scales 4).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, DEVICE, CUDA. */
+fp4moe_status fp4moe_add_rmsnorm_fp8(const uint16_t *x, int64_t x_ld, const uint16_t *residual, const uint16_t *gamma,
+                                     int32_t T, int32_t H, float eps, uint16_t *residual_out, uint16_t *y, uint8_t *q,
+                                     float *scales, void *stream);
+
+/* SwiGLU with E4M3 output: h = silu(g) * u in fp32 (silu(g) = g / (1 + e^-g)),
+ * q [T, I] and scales [T, ceil(I / 128)] its codes.  gu bf16: row t holds g in
+ * columns 0..I-1 and u in I..2I-1, row stride gu_ld elements (>= 2I, a
+ * multiple of 8).  0 <= T <= 2^20, 16 <= I <= 65536, I % 16 == 0; gu and q
+ * 16-byte aligned.  Errors as fp4moe_add_rmsnorm_fp8. */
+fp4moe_status fp4moe_swiglu_fp8(const uint16_t *gu, int64_t gu_ld, int32_t T, int32_t I, uint8_t *q, float *scales,
+                                void *stream);
+
+/* Block-scaled FP8 linear: out[t, n] = sum over K blocks b of
+ *   xs[t, b] * w_scale[n / 128, b] * sum_{k in b} xq[t, k] * w[n, k].
+ * out: bf16 (out_is_fp32 = 0) or fp32 [T, N] with row stride out_ld elements
+ * (>= N).  0 <= T <= 2^20, 16 <= K <= 65536, K % 16 == 0, 1 <= N <= 2^20.
+ * xq and w 16-byte aligned.  ws: fp4moe_linear_fp8_block_workspace_size bytes
+ * (0: unsupported sizes); it starts with a status word that each call clears
+ * and that fp4moe_get_status reads (FP4MOE_ERR_TIMEOUT: a device-side wait ran
+ * out and the output is not valid).  The result is the same on every run. */
+size_t fp4moe_linear_fp8_block_workspace_size(int32_t T, int32_t K, int32_t N);
+fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uint8_t *xq, const float *xs,
+                                      const uint8_t *w, const float *w_scale, void *out, int64_t out_ld,
+                                      int32_t out_is_fp32, void *ws, size_t ws_bytes, void *stream);
+
+/* Expert weights of fp4moe_experts_fp8_block: E4M3 codes with fp32 scales per
+ * 128 x 128 block.
+ *   w13 [E, 2I, H] (gate rows, then up rows), w13_scale [E, 2I/128, H/128];
+ *   w2 [E, H, I], w2_scale [E, H/128, I/128];
+ *   sh13, sh13_scale, sh2, sh2_scale: the shared expert (E = 1), NULL when
+ *   n_shared == 0. */
+typedef struct {
+  const uint8_t *w13;
+  const float *w13_scale;
+  const uint8_t *w2;
+  const float *w2_scale;
+  const uint8_t *sh13;
+  const float *sh13_scale;
+  const uint8_t *sh2;
+  const float *sh2_scale;
+} fp4moe_fp8_block_weights;
+
+/* The experts of a mixture-of-experts layer for few tokens (T <= 16), after
+ * the router: out[t] = sum_j topk_w[t, j] * expert_{topk_idx[t, j]}(x_t)
+ * (+ the shared expert with weight 1), bf16 [T, H], in two kernels.
+ *   [g; u] = W13 x_t;  h = silu(g) * u (fp32), requantised to E4M3 with one
+ *   scale per 128 columns;  y = W2 h;  fp32 sums, one rounding to bf16.
+ * xq [T, H], xs [T, H/128]: the quantised activations; topk_idx, topk_w
+ * [T, top_k] as fp4moe_route writes them.  A route outside [0, E) (an expert
+ * that another rank holds) adds nothing; a token without any gives zeros; an
+ * expert chosen twice by a token counts with the sum of its weights.  Only
+ * chosen experts' weights are read, each once for all its tokens.
+ * dims->fmt FP4MOE_FP8; the routing parameters of dims are not used.
+ * ws: fp4moe_experts_fp8_block_workspace_size(dims) bytes (0: unsupported).
+ * Codes, out and ws 16-byte aligned.  The result is the same on every run. */
+size_t fp4moe_experts_fp8_block_workspace_size(const fp4moe_dims *dims);
+fp4moe_status fp4moe_experts_fp8_block(const fp4moe_dims *dims, const fp4moe_fp8_block_weights *w, const uint8_t *xq,
+                                       const float *xs, const int32_t *topk_idx, const float *topk_w, uint16_t *out,
+                                       void *ws, size_t ws_bytes, void *stream);
+
 /* Exact MXFP4 -> FP8 (E4M3) per-channel conversion ("Kimi-K2.7-Code on
  * Gaudi 2", section "Exact MXFP4 to FP8 per-channel conversion").
  *   codes [rows, K/2] packed E2M1, scales [rows, K/32] E8M0 row-major ->
