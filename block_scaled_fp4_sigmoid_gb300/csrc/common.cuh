@@ -330,6 +330,17 @@ __device__ __forceinline__ void tc_mma_f8_elect(uint32_t d, uint64_t a, uint64_t
       : "memory");
 }
 
+// The same over a CTA pair (M = 256; each CTA supplies its 128 rows of A and
+// half of B's rows).
+__device__ __forceinline__ void tc_mma_f8_pair_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                     uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "@p tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // BF16 x BF16 MMA (kind::f16, K = 16 per instruction), fp32 accumulate,
 // issued by one elected lane of the calling warp.
 __device__ __forceinline__ void tc_mma_bf16_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -393,13 +404,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n) {
 }
 
 // Instruction descriptor of a dense E4M3 MMA: fp32 D, E4M3 A and B (format
-// code 0), both K-major, M = 128, N = n.
-__host__ __device__ constexpr uint32_t idesc_f8(uint32_t n) {
+// code 0), both K-major, M = m (256: a CTA pair), N = n.
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t n, uint32_t m = 128) {
   return 1u << 4              // D format: fp32
          | 0u << 7            // A format: E4M3
          | 0u << 10           // B format: E4M3
          | (n >> 3) << 17     // N / 8
-         | (128u >> 4) << 24; // M / 16
+         | (m >> 4) << 24;    // M / 16
 }
 
 // ---------------------------------------------------------------- FP4 / FP8 encoders

@@ -1,0 +1,532 @@
+// Block-scaled FP8 linear for many tokens on the tensor cores (tcgen05,
+// E4M3 x E4M3, fp32 accumulators in tensor memory).
+//
+// The scales change every 128 columns of K and are arbitrary fp32 numbers,
+// so they cannot ride in the MMA: each K block's product goes to one of two
+// tensor-memory buffers, and the epilogue warps fold it, times xs[t, b]
+// ws[n / 128, b], into fp32 sums held in their registers while the MMAs of
+// the next block fill the other buffer.  Lanes are tokens, so a thread's
+// factor is one number per block: one fused multiply-add per element.
+//
+// Work split: with about a tile or more for every SM, persistent CTAs take whole
+// tiles in turn, 256 weight rows wide where that fills whole rounds and 128
+// wide for the rest (a launch of its own that starts where the first one's
+// CTAs run out of tiles).  With fewer, a cluster of S CTAs shares a tile, each
+// with a run of its K blocks; the sums meet in distributed shared memory,
+// where each CTA adds a slice of the columns over the runs, in the order of K.
+//
+// Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 4-11 epilogue
+// (a warp group of their own, with the larger register share).  Every wait
+// is bounded; a timeout records FP4MOE_ERR_TIMEOUT in the status word, drains
+// copies and MMAs in flight, frees tensor memory and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "fp8_block.cuh"
+#include "internal.h"
+
+namespace fp4moe {
+
+namespace {
+
+// Tiles of one launch: 128 tokens x BN rows of W.
+struct TcPlan {
+  int split;              // CTAs that share a tile
+  int nb;                 // K blocks
+  int mtiles, ntiles;
+};
+constexpr int kTcCtas = 152;    // one CTA per SM
+
+struct TcParams {
+  CUtensorMap tmx, tmw;
+  const float *xs, *ws;
+  uint8_t* out;
+  int64_t out_ld;
+  int32_t* status;
+  TcPlan plan;
+  int T, N;
+  int out_fp32, vec;      // vec: 16-byte stores are aligned
+  int second;             // the second launch of a call: joins the first one's end, not its start
+};
+
+template <int BN>
+struct TcCfg {
+  static constexpr int kEpiWarps = 8, kThreads = 128 + 32 * kEpiWarps;  // warps 2 and 3 idle
+  static constexpr int kCols = BN / 2;  // columns of one epilogue warp
+  static constexpr int kABytes = 128 * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kBufs = 512 / BN;              // all of tensor memory
+  static constexpr int kStaging = kEpiWarps * 4096;   // 32 rows x 128 bytes per epilogue warp
+  static constexpr int kSmem = kStages * kStage + kStaging + 1024;
+  // launched with 168 registers a thread (384 threads); 128 x 40 + 256 x 232 = 384 x 168
+  static constexpr int kCtlRegs = 40, kEpiRegs = 232;
+};
+
+__device__ __forceinline__ uint64_t desc_sw128_k(uint32_t saddr) { return smem_desc(saddr, 16, 1024, 2); }
+
+// 16 tensor-memory columns of this thread's lane, in flight until tmem_landed16.
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Waits for every fetch of this thread; naming the registers keeps their uses behind the wait.
+__device__ __forceinline__ void tmem_landed16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+// acc += a * s, two fp32 lanes in one instruction.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(s));
+}
+
+// 16 bytes at this CTA's shared-memory offset in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// A scale load that stays where it is written (volatile): moved down to its
+// first use, its whole latency would show in every K block.
+__device__ __forceinline__ float fetch1(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// Tile order: groups of kGroupM token tiles, each group over every weight
+// tile, so that the tiles running at one time share both operands in L2.
+constexpr int kGroupM = 8;
+__device__ __forceinline__ void tile_at(int tile, int mtiles, int ntiles, int& mt, int& nt) {
+  const int per = kGroupM * ntiles, g = tile / per, in = tile - g * per;
+  const int gm = min(kGroupM, mtiles - g * kGroupM);
+  nt = in / gm;
+  mt = g * kGroupM + in - nt * gm;
+}
+
+template <int BN, bool SPLIT>
+__global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const __grid_constant__ TcParams p) {
+  using C = TcCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
+  __shared__ __align__(8) uint64_t bar_tfull[C::kBufs], bar_tempty[C::kBufs], bar_done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // SPLIT: one tile a cluster, K blocks [kb0, kb1) in this CTA; else tiles
+  // blockIdx.x, + gridDim.x, ... whole
+  const int S = SPLIT ? p.plan.split : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
+  const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S, tiles = p.plan.mtiles * p.plan.ntiles;
+  const int kb0 = SPLIT ? p.plan.nb * rank / S : 0, kb1 = SPLIT ? p.plan.nb * (rank + 1) / S : p.plan.nb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), 1);
+    }
+    for (int a = 0; a < C::kBufs; ++a) {
+      mbar_init(smem_u32(&bar_tfull[a]), 1);
+      mbar_init(smem_u32(&bar_tempty[a]), C::kEpiWarps);
+    }
+    mbar_init(smem_u32(&bar_done), 2);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&p.tmx);
+    prefetch_tmap(&p.tmw);
+  }
+  // The second launch of a call begins once every CTA of the first has passed
+  // its own wait, so its inputs are complete; it waits for the first at its end,
+  // so that whoever waits for the second waits for both.
+  if (!p.second) {
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_v = &abort_flag;
+  auto timed_out = [&]() {  // by one lane
+    if (!*abort_v) record_status(p.status, FP4MOE_ERR_TIMEOUT, ST_TIMEOUT);
+    *abort_v = 1;
+  };
+  // bounded wait with a warp-uniform outcome
+  auto wait_w = [&](uint32_t bar, uint32_t par) {
+    return __all_sync(0xffffffffu, mbar_wait_abortable(bar, par, kWaitLimitNs, abort_v)) != 0;
+  };
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kCtlRegs));
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_par = 0;
+      bool ok = true;
+      for (int tile = first; ok && tile < tiles; tile += step) {
+        int mt, nt;
+        tile_at(tile, p.plan.mtiles, p.plan.ntiles, mt, nt);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_abortable(smem_u32(&bar_empty[stage]), phase ^ 1u, kWaitLimitNs, abort_v)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&bar_full[stage]), base = sbase + stage * C::kStage;
+          mbar_arrive_expect_tx(fb, C::kStage);
+          armed |= 1u << stage;
+          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+          tma_load_2d(base, &p.tmx, fb, kb * 128, mt * 128);
+          tma_load_2d(base + C::kABytes, &p.tmw, fb, kb * 128, nt * BN);
+          if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) timed_out();
+      for (int s = 0; s < C::kStages; ++s)  // every armed stage lands before the CTA exits
+        if ((armed >> s) & 1u) (void)mbar_wait(smem_u32(&bar_full[s]), (armed_par >> s) & 1u);
+    }
+    __syncwarp();
+  } else if (warp < 3) {
+    // ------------------------------------------------------------ MMA issuers
+    // Two, for the even and the odd K blocks: issuing a block's four MMAs and
+    // its two commits takes one warp longer than the tensor core needs for it.
+    const uint64_t a0 = desc_sw128_k(sbase), b0 = desc_sw128_k(sbase + C::kABytes);
+    int stage = warp - 1, buf = warp - 1;
+    uint32_t phase = 0, bphase = 0;
+    bool ok = true;
+    int mine = warp - 1;  // K blocks to pass by before this warp's next one
+    for (int tile = first; ok && tile < tiles; tile += step) {
+      int kb = kb0 + mine;
+      for (; kb < kb1; kb += 2) {
+        if (!wait_w(smem_u32(&bar_tempty[buf]), bphase ^ 1u) || !wait_w(smem_u32(&bar_full[stage]), phase)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t so = (uint64_t)((stage * C::kStage) >> 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // K = 32 per MMA, 32 bytes of the 128-byte swizzle row
+          tc_mma_f8_elect(tmem + buf * BN, a0 + so + 2 * j, b0 + so + 2 * j, idesc_f8(BN), j ? 1u : 0u);
+        tc_commit_elect(smem_u32(&bar_empty[stage]));
+        tc_commit_elect(smem_u32(&bar_tfull[buf]));
+        stage += 2;  // stages and buffers are even in number
+        if (stage >= C::kStages) { stage -= C::kStages; phase ^= 1u; }
+        buf += 2;
+        if (buf >= C::kBufs) { buf -= C::kBufs; bphase ^= 1u; }
+      }
+      mine = kb - kb1;
+    }
+    // all issued MMAs must finish before tensor memory is released
+    tc_commit_elect(smem_u32(&bar_done));
+    (void)mbar_wait(smem_u32(&bar_done), 0);
+    if (!ok && lane == 0) timed_out();
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
+    const int q = warp & 3;                           // tensor-memory lane quadrant of this warp
+    const int c0 = ((warp - 4) >> 2) * C::kCols;      // its columns
+    uint8_t* stg = smem_raw + (sbase - smem_u32(smem_raw)) + C::kStages * C::kStage + (warp - 4) * 4096;
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + c0;
+    int buf = 0, t0 = 0, n0 = 0;
+    uint32_t bphase = 0;
+    bool ok = true;
+    const float *xs = nullptr, *ws = nullptr;
+    // the next K blocks' factors, fetched two blocks ahead (across tiles too)
+    float fx[2], fw[2];
+    auto open_tile = [&](int tile) {
+      int mt, nt;
+      tile_at(tile, p.plan.mtiles, p.plan.ntiles, mt, nt);
+      t0 = mt * 128 + 32 * q;
+      n0 = nt * BN + c0;
+      xs = p.xs + (int64_t)min(t0 + lane, p.T - 1) * p.plan.nb;
+      ws = p.ws + (int64_t)(min(n0, p.N - 1) / kBlk) * p.plan.nb;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fx[i] = fetch1(xs + min(kb0 + i, kb1 - 1)), fw[i] = fetch1(ws + min(kb0 + i, kb1 - 1));
+    };
+    uint64_t acc[C::kCols / 2];  // pairs of columns
+    if (first < tiles) open_tile(first);
+    for (int tile = first; tile < tiles; tile += step) {
+#pragma unroll
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const float f = fx[0] * fw[0];
+        const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+        fx[0] = fx[1], fw[0] = fw[1];
+        if (kb + 2 < kb1) fx[1] = fetch1(xs + kb + 2), fw[1] = fetch1(ws + kb + 2);
+        if (!wait_w(smem_u32(&bar_tfull[buf]), bphase)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[2][16];
+        tmem_fetch16(tq + buf * BN, v[0]);
+#pragma unroll
+        for (int c = 0; c < C::kCols / 16; ++c) {
+          tmem_landed16(v[c & 1]);
+          if (c + 1 < C::kCols / 16) {
+            tmem_fetch16(tq + buf * BN + 16 * (c + 1), v[(c + 1) & 1]);
+          } else {  // the buffer has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_tempty[buf]));
+            if (++buf == C::kBufs) { buf = 0; bphase ^= 1u; }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fma2(acc[8 * c + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), f2);
+        }
+      }
+      if (!ok) break;
+      if constexpr (SPLIT) break;
+      const int st0 = t0, sn0 = n0;
+      if (tile + step < tiles) open_tile(tile + step);
+      // through shared memory (16-byte pieces xor-swizzled by the row), so
+      // that a store covers whole 128-byte runs of a row
+      const int esz = p.out_fp32 ? 4 : 2, per = 128 / esz;
+#pragma unroll
+      for (int o = 0; o < C::kCols / 32; ++o) {  // 32 fp32 columns at a time; bf16 takes 64
+        if (!p.out_fp32 && o >= C::kCols / 64) break;
+        const int nc = sn0 + o * per;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[4];
+          if (p.out_fp32) {
+            unpack2(acc[16 * o + 2 * c], w[0], w[1]);
+            unpack2(acc[16 * o + 2 * c + 1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t lo, hi;
+              unpack2(acc[(32 * o + 4 * c + i) % (C::kCols / 2)], lo, hi);
+              w[i] = bf16x2_rn(__uint_as_float(lo), __uint_as_float(hi));
+            }
+          }
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        const int ncol = min(per, p.N - nc), nrow = min(32, p.T - st0);
+        uint8_t* dst = p.out + ((int64_t)st0 * p.out_ld + nc) * esz;
+        if (p.vec && ncol == per) {
+          uint8_t* d = dst + (int64_t)(lane >> 3) * p.out_ld * esz + 16 * (lane & 7);
+          const int64_t ld4 = 4 * p.out_ld * esz;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (lane >> 3) + 4 * i;
+            const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            if (r < nrow) *reinterpret_cast<uint4*>(d + i * ld4) = w;
+          }
+        } else {
+          for (int r = 0; r < nrow; ++r)
+            for (int c = lane; c < ncol; c += 32) {
+              const int at = r * 128 + ((((c * esz) >> 4) ^ (r & 7)) << 4) + ((c * esz) & 15);
+              if (p.out_fp32)
+                *reinterpret_cast<uint32_t*>(dst + ((int64_t)r * p.out_ld + c) * 4) =
+                    *reinterpret_cast<const uint32_t*>(stg + at);
+              else
+                *reinterpret_cast<uint16_t*>(dst + ((int64_t)r * p.out_ld + c) * 2) =
+                    *reinterpret_cast<const uint16_t*>(stg + at);
+            }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) timed_out();
+    __syncwarp();
+    if constexpr (SPLIT) {
+      // the pipeline's stages have been read: they take the CTA's sums,
+      // vector i (4 columns) of epilogue thread et at 16 (256 i + et)
+      const uint32_t mine = sbase + 16u * (threadIdx.x - 128);
+#pragma unroll
+      for (int i = 0; i < C::kCols / 4; ++i) {
+        uint32_t w[4];
+        unpack2(acc[2 * i], w[0], w[1]);
+        unpack2(acc[2 * i + 1], w[2], w[3]);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + 4096u * i), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3])
+                     : "memory");
+      }
+    }
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_arrive_wait();  // every CTA's sums are in its shared memory
+    if (warp >= 4 && !*abort_v) {
+      const int q = warp & 3, c0 = ((warp - 4) >> 2) * C::kCols, vs = C::kCols / 4 / S;  // vectors of this CTA's slice
+      const uint32_t at = sbase + 16u * (threadIdx.x - 128);
+      int mt, nt;
+      tile_at(first, p.plan.mtiles, p.plan.ntiles, mt, nt);
+      const int row = mt * 128 + 32 * q + lane, col = nt * BN + c0 + 4 * vs * rank;
+      const int esz = p.out_fp32 ? 4 : 2;
+      uint8_t* dst = p.out + ((int64_t)row * p.out_ld + col) * esz;
+      for (int i = 0; i < vs; i += 2) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        for (int r = 0; r < S; ++r) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 w = ld_cluster(at + 4096u * (vs * rank + i + j), r);
+            v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
+          }
+        }
+        const int n = row < p.T ? min(8, p.N - col - 4 * i) : 0;
+        if (p.vec && n == 8) {
+          if (p.out_fp32) {
+            reinterpret_cast<float4*>(dst)[i] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(dst)[i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+            *reinterpret_cast<uint4*>(dst + 8 * i) =
+                make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n) {
+              if (p.out_fp32)
+                reinterpret_cast<float*>(dst)[4 * i + j] = v[j];
+              else
+                reinterpret_cast<uint16_t*>(dst)[4 * i + j] = f32_to_bf16_rn(v[j]);
+            }
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  // (SPLIT: no CTA leaves while another reads its shared memory)
+  if constexpr (SPLIT) cluster_arrive_wait();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (p.second) pdl_wait();
+}
+
+template <int BN, bool SPLIT>
+cudaError_t launch_tc(const LinearFp8Args& a, int split, bool second, cudaStream_t s) {
+  using C = TcCfg<BN>;
+  auto k = linear_tc_kernel<BN, SPLIT>;
+  TcParams p;
+  memset(&p, 0, sizeof(p));
+  {
+    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.T}, strides[1] = {(uint64_t)a.K};
+    const uint32_t box[2] = {128, 128};
+    if (!encode_tmap_u8(&p.tmx, a.xq, 2, dims, strides, box, true)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.N}, strides[1] = {(uint64_t)a.K};
+    const uint32_t box[2] = {128, (uint32_t)BN};
+    if (!encode_tmap_u8(&p.tmw, a.w, 2, dims, strides, box, true)) return cudaErrorInvalidValue;
+  }
+  p.xs = a.xs;
+  p.ws = a.ws;
+  p.out = static_cast<uint8_t*>(a.out);
+  p.out_ld = a.out_ld;
+  p.status = static_cast<int32_t*>(a.scratch);
+  p.plan = {split, blocks128(a.K), (a.T + 127) / 128, (a.N + BN - 1) / BN};
+  p.T = a.T;
+  p.N = a.N;
+  p.out_fp32 = a.out_fp32 ? 1 : 0;
+  p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_ld * (a.out_fp32 ? 4 : 2) % 16 == 0;
+  p.second = second ? 1 : 0;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int64_t tiles = (int64_t)p.plan.mtiles * p.plan.ntiles;
+  if constexpr (SPLIT)
+    return launch_pdl_cluster(k, dim3((unsigned)(tiles * split)), dim3(C::kThreads), C::kSmem, s, (unsigned)split, p);
+  // (the second launch: a CTA per tile, taken up as the first one's CTAs leave)
+  return launch_pdl(k, dim3((unsigned)(second ? tiles : std::min<int64_t>(tiles, kTcCtas))), dim3(C::kThreads), C::kSmem, s,
+                    p);
+}
+
+// How a call is run: columns [0, wide) in tiles of 256, the rest in tiles of
+// 128; split > 1: all of it in tiles of 128 shared by `split` CTAs.  Chosen by
+// the time per K block of a tile (measured: 0.43 us 256 wide, 0.29 us 128
+// wide; joining a split tile 3 us) and the rounds that the tiles make on 152
+// SMs.  A split tile's CTAs are a cluster, and as many clusters as run at the
+// same time are taken (72 of 2, 32 of 4, 16 of 8: more would make a second
+// round, measured at twice the time).
+struct TcChoice {
+  int wide, split;
+};
+TcChoice choose(int T, int K, int N) {
+  constexpr int64_t kT256 = 43, kT128 = 29, kJoin = 300;  // 10 ns
+  const int64_t nb = blocks128(K), mt = (T + 127) / 128, sms = kTcCtas;
+  const int64_t n128 = (N + 127) / 128;
+  TcChoice best{0, 1};
+  int64_t cost = (mt * n128 + sms - 1) / sms * nb * kT128;
+  for (int split = 2; split <= 8; split *= 2) {
+    const int64_t c = (nb + split - 1) / split * kT128 + kJoin;
+    if (mt * n128 <= (split == 2 ? 72 : split == 4 ? 32 : 16) && nb >= 2 * split && c < cost) cost = c, best = {0, split};
+  }
+  for (int64_t w = (N + 255) / 256; w > 0; --w) {  // w tiles of 256, the rest of 128
+    const int64_t rest = std::max<int64_t>(0, n128 - 2 * w) * mt, t = w * mt, full = t / sms, late = t % sms;
+    // the SMs with a tile less take the first of the rest
+    const int64_t early = sms - late;
+    int64_t c = (full + (late ? 1 : 0)) * kT256;
+    if (rest > 0) {
+      const int64_t more = std::max<int64_t>(0, rest - early);
+      c = std::max(c, full * kT256 + kT128);  // (a CTA of the second launch leaves once the first has ended)
+      c += (more + sms - 1) / sms * kT128;
+    }
+    c = c * nb + (rest > 0 ? 100 : 0);  // 1 us for the second launch
+    if (c < cost) cost = c, best = {(int)std::min<int64_t>(256 * w, N), 1};
+  }
+  return best;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s) {
+  const TcChoice c = choose(a.T, a.K, a.N);
+  if (c.split > 1) return launch_tc<128, true>(a, c.split, false, s);
+  if (c.wide == 0) return launch_tc<128, false>(a, 1, false, s);
+  LinearFp8Args part = a;
+  part.N = c.wide;
+  cudaError_t e = launch_tc<256, false>(part, 1, false, s);
+  if (e != cudaSuccess || c.wide == a.N) return e;
+  part.N = a.N - c.wide;
+  part.w += (int64_t)c.wide * a.K;
+  part.ws += (int64_t)(c.wide / kBlk) * blocks128(a.K);
+  part.out = static_cast<uint8_t*>(a.out) + (int64_t)c.wide * (a.out_fp32 ? 4 : 2);
+  return launch_tc<128, false>(part, 1, true, s);
+}
+
+}  // namespace fp4moe

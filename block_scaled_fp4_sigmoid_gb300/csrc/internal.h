@@ -155,6 +155,7 @@ struct LinearFp8Args {
 };
 size_t linear_fp8_workspace(int T, int K, int N);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
+cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s);  // tensor cores
 constexpr int kExpertsMaxT = 16;
 size_t experts_fp8_workspace(const fp4moe_dims& d);
 cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weights& w, const uint8_t* xq,
