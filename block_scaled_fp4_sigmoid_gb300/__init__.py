@@ -129,6 +129,7 @@ def lib() -> ctypes.CDLL:
         L.fp4moe_linear_fp8_block_workspace_size.argtypes = [i32, i32, i32]
         L.fp4moe_linear_fp8_block_workspace_size.restype = sz
         L.fp4moe_linear_fp8_block.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i64, i32, vp, sz, vp]
+        L.fp4moe_linear_fp8_block_status.argtypes = [vp, P(i32), P(i64)]
         L.fp4moe_experts_fp8_block_workspace_size.argtypes = [P(Dims)]
         L.fp4moe_experts_fp8_block_workspace_size.restype = sz
         L.fp4moe_experts_fp8_block.argtypes = [P(Dims), P(Fp8BlockWeights), vp, vp, vp, vp, vp, vp, sz, vp]
@@ -139,6 +140,7 @@ def lib() -> ctypes.CDLL:
                      "fp4moe_clear_status",
                      "fp4moe_get_status", "fp4moe_route_noalloc", "fp4moe_route_noalloc_status",
                      "fp4moe_check_scales", "fp4moe_add_rmsnorm_fp8", "fp4moe_swiglu_fp8", "fp4moe_linear_fp8_block",
+                     "fp4moe_linear_fp8_block_status",
                      "fp4moe_experts_fp8_block"):
             getattr(L, name).restype = i32
         _LIB = L
@@ -286,9 +288,17 @@ def linear_fp8_block_workspace_size(T: int, K: int, N: int) -> int:
 
 
 def linear_fp8_block(T: int, K: int, N: int, xq: int, xs: int, w: int, w_scale: int, out: int, out_ld: int,
-                     out_is_fp32: bool, ws: int, ws_bytes: int, stream: int = 0) -> None:
+                     out_is_fp32: bool, ws: int | None, ws_bytes: int, stream: int = 0) -> None:
     _ok(lib().fp4moe_linear_fp8_block(T, K, N, xq, xs, w, w_scale, out, out_ld, int(out_is_fp32), ws, ws_bytes,
                                       stream), "fp4moe_linear_fp8_block")
+
+
+def linear_fp8_block_status(stream: int = 0) -> tuple[int, int]:
+    """Status recorded on the current device by the linear_fp8_block calls without a workspace
+    since it was last read; reading clears it."""
+    st, n = ctypes.c_int32(0), ctypes.c_int64(0)
+    _ok(lib().fp4moe_linear_fp8_block_status(stream, ctypes.byref(st), ctypes.byref(n)), "fp4moe_linear_fp8_block_status")
+    return st.value, n.value
 
 
 def experts_fp8_block_workspace_size(dims: Dims) -> int:

@@ -40,7 +40,16 @@ __device__ __forceinline__ void quant_block(const float* v, bool in, uint8_t* q,
   for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float s = e4m3_scale(amax);
   if (in) {
-    *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3], s), e4m3x4(v[4], v[5], v[6], v[7], s));
+    const float r = __fdiv_rn(1.f, s);
+    float t[8];
+    if (s >= 1.17549435e-38f) {  // (one test for the eight)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = v[j] * r;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = e4m3_scaled(v[j], s, r);
+    }
+    *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]));
     if ((threadIdx.x & 15) == 0) *scale = s;
   }
 }
@@ -194,10 +203,10 @@ size_t fp4moe_linear_fp8_block_workspace_size(int32_t T, int32_t K, int32_t N) {
 fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uint8_t* xq, const float* xs,
                                       const uint8_t* w, const float* w_scale, void* out, int64_t out_ld,
                                       int32_t out_is_fp32, void* ws, size_t ws_bytes, void* stream) {
-  if (!xq || !xs || !w || !w_scale || !out || !ws) return FP4MOE_ERR_INVALID_ARG;
+  if (!xq || !xs || !w || !w_scale || !out) return FP4MOE_ERR_INVALID_ARG;
   const size_t need = fp4moe_linear_fp8_block_workspace_size(T, K, N);
   if (need == 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
-  if (ws_bytes < need) return FP4MOE_ERR_WORKSPACE;
+  if (ws ? ws_bytes < need : ws_bytes != 0) return FP4MOE_ERR_WORKSPACE;
   if (out_ld < N || !aligned(xq, 16) || !aligned(w, 16) || !aligned(xs, 4) || !aligned(w_scale, 4) ||
       !aligned(out, out_is_fp32 ? 4 : 2) || !aligned(ws, 16))
     return FP4MOE_ERR_INVALID_ARG;
@@ -205,6 +214,14 @@ fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uin
   if (fp4moe_status st = check_device()) return st;
   const LinearFp8Args a{T, K, N, xq, xs, w, w_scale, out, out_ld, out_is_fp32 != 0, ws};
   return cuda_status(launch_linear_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp4moe_status fp4moe_linear_fp8_block_status(void* stream, fp4moe_status* st, int64_t* count) {
+  if (fp4moe_status e = check_device()) return e;
+  int32_t* word = nullptr;
+  if (linear_fp8_status_word(&word) != cudaSuccess) return FP4MOE_ERR_CUDA;
+  const fp4moe_status e = fp4moe_get_status(word, stream, st, count);
+  return e ? e : fp4moe_clear_status(word, stream);
 }
 
 size_t fp4moe_experts_fp8_block_workspace_size(const fp4moe_dims* dims) {

@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kGuThreads) experts_gateup_kernel(const Expert
 #pragma unroll
           for (int q = 1; q < 8; ++q) a = max_nan(a, amax[q][tok]);
           const float s = e4m3_scale(a);
-          const uint32_t two = e4m3x4(h[i][c], h[i][c + 2], 0.f, 0.f, s);
+          const float r = __fdiv_rn(1.f, s);
+          const uint32_t two = e4m3x4(e4m3_scaled(h[i][c], s, r), e4m3_scaled(h[i][c + 2], s, r), 0.f, 0.f);
           codes[tok][16 * rg + g] = (uint8_t)two;
           codes[tok][16 * rg + g + 8] = (uint8_t)(two >> 8);
           if (rg == 0 && g == 0 && ((mask >> tok) & 1u)) p.hs[(int64_t)(u * p.T + tok) * ib + b] = s;

@@ -13,7 +13,7 @@ struct StreamParams {
   const float *xs, *ws;
   void* out;
   int64_t out_ld;
-  int32_t* status;  // cleared here; this kernel waits for nothing
+  int32_t* status;  // nullable; cleared here (this kernel waits for nothing)
   int T, K, N, out_fp32;
 };
 
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
   __shared__ float part[kStreamWarps][NT * 4][32];
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
+  if (p.status && blockIdx.x == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * 16, nb = blocks128(p.K);
   const float* ws = p.ws + (int64_t)(n0 / kBlk) * nb;

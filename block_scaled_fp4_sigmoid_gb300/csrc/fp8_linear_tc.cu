@@ -31,6 +31,9 @@ namespace fp4moe {
 
 namespace {
 
+// Where calls without a workspace record a timeout; cleared when it is read.
+__device__ int32_t linear_status[kStatusInts];
+
 // Tiles of one launch: 128 tokens x BN rows of W.
 struct TcPlan {
   int split;              // CTAs that share a tile
@@ -44,7 +47,7 @@ struct TcParams {
   const float *xs, *ws;
   uint8_t* out;
   int64_t out_ld;
-  int32_t* status;
+  int32_t* status;        // null: linear_status
   TcPlan plan;
   int T, N;
   int out_fp32, vec;      // vec: 16-byte stores are aligned
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
   // so that whoever waits for the second waits for both.
   if (!p.second) {
     pdl_wait();
-    if (blockIdx.x == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
+    if (p.status && blockIdx.x == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
   }
   pdl_trigger();
   tc_fence_before();
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
   const uint32_t tmem = tmem_slot;
   volatile int* abort_v = &abort_flag;
   auto timed_out = [&]() {  // by one lane
-    if (!*abort_v) record_status(p.status, FP4MOE_ERR_TIMEOUT, ST_TIMEOUT);
+    if (!*abort_v) record_status(p.status ? p.status : linear_status, FP4MOE_ERR_TIMEOUT, ST_TIMEOUT);
     *abort_v = 1;
   };
   // bounded wait with a warp-uniform outcome
@@ -513,6 +516,13 @@ TcChoice choose(int T, int K, int N) {
 }
 
 }  // namespace
+
+cudaError_t linear_fp8_status_word(int32_t** word) {
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, linear_status);
+  *word = static_cast<int32_t*>(p);
+  return e;
+}
 
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s) {
   const TcChoice c = choose(a.T, a.K, a.N);

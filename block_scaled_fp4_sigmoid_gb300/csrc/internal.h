@@ -151,8 +151,9 @@ struct LinearFp8Args {
   void* out;
   int64_t out_ld;
   bool out_fp32;
-  void* scratch;
+  void* scratch;  // nullable: the status word of this call
 };
+cudaError_t linear_fp8_status_word(int32_t** word);  // the current device's, of the calls without one
 size_t linear_fp8_workspace(int T, int K, int N);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s);  // tensor cores

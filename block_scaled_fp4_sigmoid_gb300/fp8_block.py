@@ -12,12 +12,13 @@ from __future__ import annotations
 import torch
 
 from . import (FP8, Dims, Fp8BlockWeights, add_rmsnorm_fp8 as _add_rmsnorm, experts_fp8_block as _experts,
-               experts_fp8_block_workspace_size, linear_fp8_block as _linear, linear_fp8_block_workspace_size,
+               experts_fp8_block_workspace_size, linear_fp8_block as _linear,
                make_dims, route as _route, swiglu_fp8 as _swiglu, workspace_size)
 
 BLOCK = 128
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_OUT = _BF16 + _F32
 
 
 def _blocks(n: int) -> int:
@@ -29,10 +30,11 @@ def _ptr(t):
 
 
 def _check(name, t, shape, dtypes, device, dense=True):
-    """A tensor of the given shape, one of the types and the device; dense (row-major)
-    or, for a matrix, with unit stride along its rows."""
-    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device:
-        raise ValueError(f"{name}: expected {shape} of {dtypes} on {device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+    """A tensor of the given shape, one of the types and the device (an index); dense
+    (row-major) or, for a matrix, with unit stride along its rows."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} of {dtypes} on cuda:{device}, got {tuple(t.shape)} of {t.dtype} "
+                         f"on {t.device}")
     if not (t.is_contiguous() if dense else t.stride(1) == 1 or t.shape[1] <= 1):
         raise ValueError(f"{name}: {'row-major' if dense else 'unit column stride'} expected, strides are {t.stride()}")
 
@@ -44,13 +46,21 @@ def _ld(t):
 
 def _out(name, t, shape, dtypes, device, dense=True):
     if t is None:
-        return torch.empty(shape, dtype=dtypes[0], device=device)
+        return torch.empty(shape, dtype=dtypes[0], device=f"cuda:{device}")
     _check(name, t, shape, dtypes, device, dense)
     return t
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _device(t):
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("CUDA tensors expected")
+    return d
+
+
+# the raw handle of a device's current stream, without a Stream object around it
+_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None, q=None, scales=None,
@@ -62,7 +72,7 @@ def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None
     if x.dim() != 2:
         raise ValueError(f"x: a matrix expected, got {tuple(x.shape)}")
     T, H = x.shape
-    dev = x.device
+    dev = _device(x)
     _check("x", x, (T, H), _BF16, dev, dense=False)
     _check("gamma", gamma, (H,), _BF16, dev)
     if residual is not None:
@@ -86,7 +96,7 @@ def swiglu_fp8(gu, *, q=None, scales=None):
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError(f"gu: [T, 2I] expected, got {tuple(gu.shape)}")
     T, I = gu.shape[0], gu.shape[1] // 2
-    dev = gu.device
+    dev = _device(gu)
     _check("gu", gu, (T, 2 * I), _BF16, dev, dense=False)
     q = _out("q", q, (T, I), _CODES, dev)
     scales = _out("scales", scales, (T, _blocks(I)), _F32, dev)
@@ -98,25 +108,23 @@ def swiglu_fp8(gu, *, q=None, scales=None):
 def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, ws=None):
     """out [T, N] = x . W^T for codes xq [T, K] with scales xs [T, K/128] and w [N, K] with
     w_scale [N/128, K/128] (fp4moe_linear_fp8_block; blocks rounded up).  out: bf16 or fp32,
-    rows may be strided.  ws: a uint8 tensor of linear_fp8_block_workspace_size(T, K, N) bytes,
-    or None (allocated here); its status word is read by get_status."""
+    rows may be strided.  ws: None, or a uint8 tensor of linear_fp8_block_workspace_size(T, K, N)
+    bytes whose status word get_status reads; without it a device-side timeout is recorded in
+    the library's word, which linear_fp8_block_status reads."""
     if xq.dim() != 2 or w.dim() != 2:
         raise ValueError(f"xq and w: matrices expected, got {tuple(xq.shape)} and {tuple(w.shape)}")
     (T, K), N = xq.shape, w.shape[0]
-    dev = xq.device
+    dev = _device(xq)
     _check("xq", xq, (T, K), _CODES, dev)
     _check("xs", xs, (T, _blocks(K)), _F32, dev)
     _check("w", w, (N, K), _CODES, dev)
     _check("w_scale", w_scale, (_blocks(N), _blocks(K)), _F32, dev)
-    out = _out("out", out, (T, N), (out_dtype,) if out is None else _BF16 + _F32, dev, dense=False)
-    if out.dtype not in _BF16 + _F32:
-        raise ValueError(f"out: bf16 or fp32, got {out.dtype}")
+    if out_dtype not in _OUT:
+        raise ValueError(f"out_dtype: bf16 or fp32, got {out_dtype}")
+    out = _out("out", out, (T, N), (out_dtype,) if out is None else _OUT, dev, dense=False)
     if T:
-        n = linear_fp8_block_workspace_size(T, K, N)
-        if ws is None:
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
         _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), _ld(out),
-                out.dtype == torch.float32, ws.data_ptr(), ws.numel(), _stream(dev))
+                out.dtype == torch.float32, _ptr(ws), ws.numel() if ws is not None else 0, _stream(dev))
     return out
 
 
@@ -130,7 +138,7 @@ def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh
         raise ValueError(f"xq, topk_idx, w13: two, two and three dimensions expected, got {tuple(xq.shape)}, "
                          f"{tuple(topk_idx.shape)}, {tuple(w13.shape)}")
     (T, H), k, E, I = xq.shape, topk_idx.shape[1], w13.shape[0], w13.shape[1] // 2
-    dev = xq.device
+    dev = _device(xq)
     _check("xq", xq, (T, H), _CODES, dev)
     _check("xs", xs, (T, _blocks(H)), _F32, dev)
     _check("topk_idx", topk_idx, (T, k), (torch.int32,), dev)
@@ -149,7 +157,7 @@ def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh
     n = experts_fp8_block_workspace_size(dims)
     out = _out("out", out, (T, H), _BF16, dev)
     if ws is None:
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        ws = torch.empty(n, dtype=torch.uint8, device=xq.device)
     weights = Fp8BlockWeights(w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), _ptr(sh13),
                               _ptr(sh13_scale), _ptr(sh2), _ptr(sh2_scale))
     _experts(dims, weights, xq.data_ptr(), xs.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(),
@@ -188,8 +196,8 @@ class Fp8BlockMoE:
         self.dims, self.gamma, self.w_router, self.bias, self.eps = dims, gamma, w_router, bias, eps
         self.weights = (w13, w13_scale, w2, w2_scale, sh13, sh13_scale, sh2, sh2_scale)
         self.device = w13.device
-        _check("w_router", w_router, (dims.E, dims.H), _BF16, self.device)
-        _check("bias", bias, (dims.E,), _F32, self.device)
+        _check("w_router", w_router, (dims.E, dims.H), _BF16, _device(w13))
+        _check("bias", bias, (dims.E,), _F32, _device(w13))
         self.ws_bytes = workspace_size(dims)  # of the router
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self.experts_ws = torch.empty(experts_fp8_block_workspace_size(dims), dtype=torch.uint8, device=self.device)
@@ -197,11 +205,12 @@ class Fp8BlockMoE:
     def route(self, y):
         """(topk_idx, topk_w) of the bf16 rows y [T, H]."""
         d = self.dims
-        _check("y", y, (d.T, d.H), _BF16, self.device)
+        dev = _device(y)
+        _check("y", y, (d.T, d.H), _BF16, dev)
         idx = torch.empty((d.T, d.top_k), dtype=torch.int32, device=self.device)
         w = torch.empty((d.T, d.top_k), dtype=torch.float32, device=self.device)
         _route(d, y.data_ptr(), self.w_router.data_ptr(), self.bias.data_ptr(), idx.data_ptr(), w.data_ptr(), None,
-               self.ws.data_ptr(), self.ws_bytes, _stream(self.device))
+               self.ws.data_ptr(), self.ws_bytes, _stream(dev))
         return idx, w
 
     def forward(self, x, residual=None):

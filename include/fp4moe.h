@@ -429,8 +429,9 @@ fp4moe_status fp4moe_linear(int32_t fmt, int32_t T, int32_t K, int32_t N, const 
  * q[t, c] * scale[t, c / 128].  Weights: E4M3 codes [N, K] row-major with fp32
  * scales [ceil(N / 128), ceil(K / 128)], one per 128 x 128 block (the last
  * blocks may be partial).  The quantising calls use scale = fp32(amax / 448)
- * and code = RNE_E4M3(fp32(v / scale)); a block of zeros has scale 0 and
- * signed zeros; a NaN in a block makes its scale NaN.
+ * and code = RNE_E4M3(fp32(v * fp32(1 / scale))), saturating (scales below
+ * the normal range: fp32(v / scale)); a block of zeros has scale 0 and signed
+ * zeros; a NaN in a block makes its scale NaN.
  * Every sum, norm and scale product is held in fp32. */
 
 /* Residual addition, RMS norm and E4M3 quantisation in one pass over a row:
@@ -462,13 +463,21 @@ fp4moe_status fp4moe_swiglu_fp8(const uint16_t *gu, int64_t gu_ld, int32_t T, in
  * out: bf16 (out_is_fp32 = 0) or fp32 [T, N] with row stride out_ld elements
  * (>= N).  0 <= T <= 2^20, 16 <= K <= 65536, K % 16 == 0, 1 <= N <= 2^20.
  * xq and w 16-byte aligned.  ws: fp4moe_linear_fp8_block_workspace_size bytes
- * (0: unsupported sizes); it starts with a status word that each call clears
- * and that fp4moe_get_status reads (FP4MOE_ERR_TIMEOUT: a device-side wait ran
- * out and the output is not valid).  The result is the same on every run. */
+ * (0: unsupported sizes), the status word that each call clears and that
+ * fp4moe_get_status reads (FP4MOE_ERR_TIMEOUT: a device-side wait ran out and
+ * the output is not valid); or NULL with ws_bytes 0: such a condition is then
+ * recorded in a word of the library's, one for each device, which
+ * fp4moe_linear_fp8_block_status reads and clears.  The result is the same on
+ * every run. */
 size_t fp4moe_linear_fp8_block_workspace_size(int32_t T, int32_t K, int32_t N);
 fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uint8_t *xq, const float *xs,
                                       const uint8_t *w, const float *w_scale, void *out, int64_t out_ld,
                                       int32_t out_is_fp32, void *ws, size_t ws_bytes, void *stream);
+
+/* Synchronises `stream`, reads and clears what the fp4moe_linear_fp8_block
+ * calls without a workspace have recorded on the current device: *st the first
+ * condition (FP4MOE_OK if none), *count how many.  Either output may be NULL. */
+fp4moe_status fp4moe_linear_fp8_block_status(void *stream, fp4moe_status *st, int64_t *count);
 
 /* Expert weights of fp4moe_experts_fp8_block: E4M3 codes with fp32 scales per
  * 128 x 128 block.

@@ -46,10 +46,10 @@ def test_swiglu_arguments(lib, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(xq=None), INVALID), (dict(ws=None), INVALID), (dict(out=None), INVALID), (dict(K=24), SHAPE), (dict(K=0), SHAPE),
+    (dict(xq=None), INVALID), (dict(ws=None), WORKSPACE), (dict(out=None), INVALID), (dict(K=24), SHAPE), (dict(K=0), SHAPE),
     (dict(N=0), SHAPE), (dict(T=-1), SHAPE), (dict(ws_bytes=16), WORKSPACE), (dict(out_ld=127), INVALID),
     (dict(xq=P + 8), INVALID), (dict(w=P + 1), INVALID), (dict(out=P + 1), INVALID),
-    (dict(out=P + 2, out_is_fp32=1), INVALID), (dict(T=0), OK)])
+    (dict(out=P + 2, out_is_fp32=1), INVALID), (dict(T=0), OK), (dict(T=0, ws=None, ws_bytes=0), OK)])
 def test_linear_arguments(lib, kw, code):
     a = dict(T=4, K=256, N=128, xq=P, xs=P, w=P, w_scale=P, out=P, out_ld=128, out_is_fp32=0, ws=P, ws_bytes=1 << 30)
     a.update(kw)
