@@ -1,9 +1,11 @@
 // Block-scaled FP8 experts for few tokens, in two kernels: gate/up + SwiGLU +
 // E4M3 requantisation, then down + weighted combine.
 //
-// Every column of the MMAs is a token (8 NT columns for up to 16 tokens), so
-// an expert's weights are read once for all its tokens, and both kernels only
-// visit experts that some token chose.
+// The columns of the MMAs are tokens: an entry of the list is a chosen expert
+// with up to 8 of the tokens that chose it (T <= 8: column = token; more
+// tokens: the set ones in order, two entries where more than 8 chose it), so
+// an expert's weights are read once for 8 tokens, and both kernels only visit
+// experts that some token chose.
 #include <algorithm>
 
 #include "fp8_block.cuh"
@@ -14,22 +16,26 @@ namespace fp4moe {
 namespace {
 
 constexpr int kMaxE = 512, kMaxTok = kExpertsMaxT, kMaxRoutes = 16 * kMaxTok;
-constexpr int kMaxList = kMaxRoutes + 1;  // chosen experts and the shared one
+constexpr int kMaxList = kMaxRoutes + 2;  // entries: at most one a route, and the shared expert's two
+constexpr int kNoTok = 255;
 
 struct ExpertsParams {
   const uint8_t *xq, *w13, *w2, *sh13, *sh2;
   const float *xs, *s13, *s2, *ss13, *ss2;
   const int32_t* idx;
   const float* wts;
-  uint8_t* hq;   // [list position * T + token, I]
-  float* hs;     // [list position * T + token, I / 128]
+  uint8_t* hq;   // [entry * 8 + column, I]
+  float* hs;     // [entry * 8 + column, I / 128]
   uint16_t* out;
   int T, H, I, E, k, shared;
 };
 
 struct ExpertList {
-  uint32_t mask[kMaxE + 1];  // tokens that chose the expert
-  uint16_t e[kMaxList];      // chosen experts, ascending; the shared one is E
+  uint32_t mask[kMaxE + 1];    // tokens that chose the expert
+  uint16_t e[kMaxList];        // entries by ascending expert; the shared one is E
+  uint8_t tok[kMaxList][8];    // token of each column, or kNoTok
+  uint8_t cols[kMaxList];      // bit c: column c has a token
+  int16_t route[kMaxRoutes];   // expert of each (token, slot), -1: none here
   int n;
 };
 
@@ -40,35 +46,61 @@ __device__ __forceinline__ void list_experts(const ExpertsParams& p, ExpertList&
   __syncthreads();
   for (int r = threadIdx.x; r < p.T * p.k; r += blockDim.x) {
     const int e = p.idx[r];
-    if (e >= 0 && e < p.E) atomicOr(&L.mask[e], 1u << (r / p.k));
+    const bool in = e >= 0 && e < p.E;
+    L.route[r] = (int16_t)(in ? e : -1);
+    if (in) atomicOr(&L.mask[e], 1u << (r / p.k));
   }
   if (threadIdx.x == 0 && p.shared) L.mask[p.E] = (1u << p.T) - 1u;
   __syncthreads();
   if (threadIdx.x < 32) {
     int n = 0;
+    const uint32_t below = (1u << threadIdx.x) - 1u;
     for (int e0 = 0; e0 <= p.E; e0 += 32) {
       const int e = e0 + threadIdx.x;
-      const bool on = e <= p.E && L.mask[e] != 0u;
-      const uint32_t m = __ballot_sync(0xffffffffu, on);
-      if (on) L.e[n + __popc(m & ((1u << threadIdx.x) - 1u))] = (uint16_t)e;
-      n += __popc(m);
+      const int cnt = e <= p.E ? __popc(L.mask[e]) : 0;
+      const uint32_t one = __ballot_sync(0xffffffffu, cnt > 0), two = __ballot_sync(0xffffffffu, cnt > 8);
+      const int at = n + __popc(one & below) + __popc(two & below);
+      if (cnt > 0) L.e[at] = (uint16_t)e;
+      if (cnt > 8) L.e[at + 1] = (uint16_t)e;
+      n += __popc(one) + __popc(two);
     }
     if (threadIdx.x == 0) L.n = n;
+  }
+  __syncthreads();
+  for (int o = threadIdx.x; o < L.n * 8; o += blockDim.x) {
+    const int u = o >> 3, c = o & 7, e = L.e[u];
+    uint32_t m = L.mask[e];
+    int tok = kNoTok;
+    if (p.T <= 8) {
+      if ((m >> c) & 1u) tok = c;
+    } else {  // the set bit of this place; an expert's second entry goes on after eight
+      const int nth = c + (u > 0 && L.e[u - 1] == e ? 8 : 0);
+      if (nth < __popc(m)) {
+        for (int i = 0; i < nth; ++i) m &= m - 1u;
+        tok = __ffs(m) - 1;
+      }
+    }
+    L.tok[u][c] = (uint8_t)tok;
+    if (c == 0) {
+      const int n = __popc(L.mask[e]), before = p.T > 8 && u > 0 && L.e[u - 1] == e ? 8 : 0;
+      L.cols[u] = (uint8_t)(p.T <= 8 ? L.mask[e] : (1u << min(8, n - before)) - 1u);
+    }
   }
   __syncthreads();
 }
 
 constexpr int kGuThreads = 512;
 
-// One unit: 128 gate and 128 up rows (one scale block of h) of one expert.
+// One unit: 128 gate and 128 up rows (one scale block of h) of one entry.
 // Warp = 16 gate rows and the 16 up rows of the same h values, over every
-// second K block.
-template <int NT>
-__global__ void __launch_bounds__(kGuThreads) experts_gateup_kernel(const ExpertsParams p) {
+// second K block, straight from global memory into mma.sync operands: 8 loads
+// of 16 bytes in flight a lane.  HBM bound: 8 tokens over 384 experts (1.75
+// GB) in 262 us, 6.7 TB/s.
+__global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const ExpertsParams p) {
   __shared__ ExpertList L;
-  __shared__ float part[8][8 * NT][32];
-  __shared__ float amax[8][8 * NT];
-  __shared__ __align__(16) uint8_t codes[8 * NT][128];  // read as 16-byte words
+  __shared__ float part[8][8][32];
+  __shared__ float amax[8][8];
+  __shared__ __align__(16) uint8_t codes[8][128];  // read as 16-byte words
   pdl_wait();
   pdl_trigger();
   list_experts(p, L);
@@ -77,17 +109,19 @@ __global__ void __launch_bounds__(kGuThreads) experts_gateup_kernel(const Expert
   const int hb = p.H / kBlk, ib = p.I / kBlk, units = L.n * ib;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int u = unit / ib, b = unit - u * ib, e = L.e[u];
-    const uint32_t mask = L.mask[e];
     const bool sh = e == p.E;
     const uint8_t* w = sh ? p.sh13 : p.w13 + (int64_t)e * 2 * p.I * p.H;
     const float* ws = sh ? p.ss13 : p.s13 + (int64_t)e * 2 * ib * hb;
     const uint8_t* row = w + (int64_t)(b * kBlk + 16 * rg + g) * p.H;
     const float *wsg = ws + (int64_t)b * hb, *wsu = ws + (int64_t)(ib + b) * hb;
-    float acc[2][NT][4];
+    // columns without a token compute token 0's values, which go nowhere
+    auto tok_of = [&](int c) { return L.tok[u][c] == kNoTok ? 0 : (int)L.tok[u][c]; };
+    const uint8_t* xr = p.xq + (int64_t)tok_of(g) * p.H;
+    const float *xs0 = p.xs + (int64_t)tok_of(2 * t) * hb, *xs1 = p.xs + (int64_t)tok_of(2 * t + 1) * hb;
+    float acc[2][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
+    for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+#pragma unroll 1
     for (int kb = kh; kb < hb; kb += 2) {
       uint4 wv[2][4], x[2];
       const int64_t k0 = kb * kBlk + 16 * t;
@@ -96,24 +130,19 @@ __global__ void __launch_bounds__(kGuThreads) experts_gateup_kernel(const Expert
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           wv[m][j] = ldg_stream(row + (int64_t)(m * p.I + 8 * (j >> 1)) * p.H + k0 + 64 * (j & 1));
-      const float sg = wsg[kb], su = wsu[kb];
+      const float sw[2] = {wsg[kb], wsu[kb]};
+      x[0] = *reinterpret_cast<const uint4*>(xr + k0);
+      x[1] = *reinterpret_cast<const uint4*>(xr + k0 + 64);
+      const float x0 = xs0[kb], x1 = xs1[kb];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint8_t* xr = p.xq + (int64_t)min(8 * i + g, p.T - 1) * p.H + k0;
-        x[0] = *reinterpret_cast<const uint4*>(xr);
-        x[1] = *reinterpret_cast<const uint4*>(xr + 64);
-        const float x0 = p.xs[min(8 * i + 2 * t, p.T - 1) * hb + kb];
-        const float x1 = p.xs[min(8 * i + 2 * t + 1, p.T - 1) * hb + kb];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_block(d, wv[m], x);
-          const float sw = m ? su : sg, s0 = sw * x0, s1 = sw * x1;
-          acc[m][i][0] = fmaf(s0, d[0], acc[m][i][0]);
-          acc[m][i][1] = fmaf(s1, d[1], acc[m][i][1]);
-          acc[m][i][2] = fmaf(s0, d[2], acc[m][i][2]);
-          acc[m][i][3] = fmaf(s1, d[3], acc[m][i][3]);
-        }
+      for (int m = 0; m < 2; ++m) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_block(d, wv[m], x);
+        const float s0 = sw[m] * x0, s1 = sw[m] * x1;
+        acc[m][0] = fmaf(s0, d[0], acc[m][0]);
+        acc[m][1] = fmaf(s1, d[1], acc[m][1]);
+        acc[m][2] = fmaf(s0, d[2], acc[m][2]);
+        acc[m][3] = fmaf(s1, d[3], acc[m][3]);
       }
     }
     // the odd K blocks' sums join the even ones'
@@ -121,52 +150,43 @@ __global__ void __launch_bounds__(kGuThreads) experts_gateup_kernel(const Expert
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[rg][(m * NT + i) * 4 + j][lane] = acc[m][i][j];
+        for (int j = 0; j < 4; ++j) part[rg][m * 4 + j][lane] = acc[m][j];
     }
     __syncthreads();
-    float h[NT][4];
+    float h[4];
     if (!kh) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int j = 0; j < 4; ++j) h[j] = swiglu(acc[0][j] + part[rg][j][lane], acc[1][j] + part[rg][4 + j][lane]);
+      // columns 2t (j = 0, 2) and 2t + 1: largest |h| over the warp's 16 rows
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h[i][j] = swiglu(acc[0][i][j] + part[rg][i * 4 + j][lane], acc[1][i][j] + part[rg][(NT + i) * 4 + j][lane]);
-        // columns 2t (j = 0, 2) and 2t + 1: largest |h| over the warp's 16 rows
+      for (int c = 0; c < 2; ++c) {
+        float a = max_nan(fabsf(h[c]), fabsf(h[c + 2]));
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float a = max_nan(fabsf(h[i][c]), fabsf(h[i][c + 2]));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-          if (g == 0) amax[rg][8 * i + 2 * t + c] = a;
-        }
+        for (int o = 4; o < 32; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if (g == 0) amax[rg][2 * t + c] = a;
       }
     }
     __syncthreads();
     if (!kh) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int c = 0; c < 2; ++c) {
+        const int col = 2 * t + c;
+        float a = amax[0][col];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int tok = 8 * i + 2 * t + c;
-          float a = amax[0][tok];
-#pragma unroll
-          for (int q = 1; q < 8; ++q) a = max_nan(a, amax[q][tok]);
-          const float s = e4m3_scale(a);
-          const float r = __fdiv_rn(1.f, s);
-          const uint32_t two = e4m3x4(e4m3_scaled(h[i][c], s, r), e4m3_scaled(h[i][c + 2], s, r), 0.f, 0.f);
-          codes[tok][16 * rg + g] = (uint8_t)two;
-          codes[tok][16 * rg + g + 8] = (uint8_t)(two >> 8);
-          if (rg == 0 && g == 0 && ((mask >> tok) & 1u)) p.hs[(int64_t)(u * p.T + tok) * ib + b] = s;
-        }
+        for (int q = 1; q < 8; ++q) a = max_nan(a, amax[q][col]);
+        const float s = e4m3_scale(a), r = __fdiv_rn(1.f, s);
+        const uint32_t two = e4m3x4(e4m3_scaled(h[c], s, r), e4m3_scaled(h[c + 2], s, r), 0.f, 0.f);
+        codes[col][16 * rg + g] = (uint8_t)two;
+        codes[col][16 * rg + g + 8] = (uint8_t)(two >> 8);
+        if (rg == 0 && g == 0) p.hs[(int64_t)(u * 8 + col) * ib + b] = s;
+      }
     }
     __syncthreads();
-    for (int o = threadIdx.x; o < 8 * NT * 8; o += kGuThreads) {
-      const int tok = o >> 3, c = 16 * (o & 7);
-      if ((mask >> tok) & 1u)
-        *reinterpret_cast<uint4*>(p.hq + (int64_t)(u * p.T + tok) * p.I + b * kBlk + c) =
-            *reinterpret_cast<const uint4*>(&codes[tok][c]);
+    for (int o = threadIdx.x; o < 64; o += kGuThreads) {
+      const int col = o >> 3, c = 16 * (o & 7);
+      if (L.tok[u][col] != kNoTok)
+        *reinterpret_cast<uint4*>(p.hq + (int64_t)(u * 8 + col) * p.I + b * kBlk + c) =
+            *reinterpret_cast<const uint4*>(&codes[col][c]);
     }
   }
 }
@@ -174,101 +194,129 @@ __global__ void __launch_bounds__(kGuThreads) experts_gateup_kernel(const Expert
 constexpr int kDnWarps = 8;
 
 // One CTA: 16 output columns (rows of every chosen expert's W2), all tokens.
-// The (expert, K block) pairs go to the warps in turn; each adds weight *
-// scales * product into its token columns, and the warps' sums are joined in
-// warp order, so the result does not depend on timing.
-template <int NT>
-__global__ void __launch_bounds__(32 * kDnWarps) experts_down_kernel(const ExpertsParams p) {
+// Runs of two K blocks go to the warps in turn, over all entries; a warp adds
+// weight * scales * product to its token columns, and the warps' sums are
+// joined in warp order, so the result does not depend on timing.  A warp's sums
+// are in registers where column = token (T <= 8), else in its own shared memory
+// (GATHER).
+//
+// HBM bound, 6.6 TB/s over both kernels at 8 tokens and 384 experts (398 us for
+// 2.6 GB).  All loads of a run are issued together, 24 warps an SM: with one K
+// block a run the call took 428 us, with four (16 warps) 421, with one prefetched
+// a block ahead 435, with blocks copied ahead into shared memory by cp.async 485
+// and more.
+//
+// The gate/up kernel has passed its own wait before this one can start, so all
+// but its output (h) is complete: the list and the routing weights are made
+// before the wait.
+template <bool GATHER>
+__global__ void __launch_bounds__(32 * kDnWarps, 3) experts_down_kernel(const ExpertsParams p) {
   __shared__ ExpertList L;
-  __shared__ float rw[kMaxList][8 * NT];  // routing weight of (list position, token)
-  __shared__ float part[kDnWarps][NT * 4][32];
+  __shared__ float rw[kMaxList][8];  // routing weight of (entry, column)
+  __shared__ float sums[kDnWarps][16][GATHER ? 17 : 9];  // row, token
+  list_experts(p, L);
+  for (int o = threadIdx.x; o < L.n * 8; o += blockDim.x) {
+    const int u = o >> 3, tok = L.tok[u][o & 7], e = L.e[u];
+    float v = 0.f;
+    if (tok != kNoTok) {
+      if (e == p.E) v = 1.f;
+      else
+        for (int j = 0; j < p.k; ++j)  // (an expert chosen twice: its weights add)
+          if (L.route[tok * p.k + j] == e) v += p.wts[tok * p.k + j];
+    }
+    rw[u][o & 7] = v;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if constexpr (GATHER)
+    for (int o = lane; o < 16 * 17; o += 32) sums[warp][0][o] = 0.f;
+  __syncthreads();
+  const int n0 = blockIdx.x * 16, hb = p.H / kBlk, ib = p.I / kBlk;
+  const int64_t wat = (int64_t)(n0 + g) * p.I + 16 * t, sat = (int64_t)(n0 / kBlk) * ib;  // into an expert's weights, scales
+  constexpr int kRun = 2;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  // a warp takes every kDnWarps-th run of kRun K blocks, over all entries
+  const int runs = (ib + kRun - 1) / kRun;
+  int u = 0, r = warp;
   pdl_wait();
   pdl_trigger();
-  list_experts(p, L);
-  for (int o = threadIdx.x; o < L.n * 8 * NT; o += blockDim.x) {
-    const int u = o / (8 * NT), tok = o - u * 8 * NT, e = L.e[u];
-    float v = 0.f;
-    if (tok < p.T) {
-      if (e == p.E)
-        v = 1.f;
-      else
-        for (int j = 0; j < p.k; ++j)
-          if (p.idx[tok * p.k + j] == e) v += p.wts[tok * p.k + j];
-    }
-    rw[u][tok] = v;
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16, hb = p.H / kBlk, ib = p.I / kBlk, items = L.n * ib;
-  float acc[NT][4];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  for (int it = warp; it < items; it += kDnWarps) {
-    const int u = it / ib, b = it - u * ib, e = L.e[u];
-    const uint32_t mask = L.mask[e];
+  for (;; r += kDnWarps) {
+    while (r >= runs) r -= runs, ++u;
+    if (u >= L.n) break;
+    const int e = L.e[u], b0 = r * kRun;
+    const uint32_t cols = L.cols[u];
     const bool sh = e == p.E;
-    const uint8_t* w = (sh ? p.sh2 : p.w2 + (int64_t)e * p.H * p.I) + (int64_t)(n0 + g) * p.I + b * kBlk + 16 * t;
-    const float sw = (sh ? p.ss2 : p.s2 + (int64_t)e * hb * ib)[(n0 / kBlk) * ib + b];
-    uint4 wv[4], x[2];
+    const uint8_t* w = (sh ? p.sh2 : p.w2 + (int64_t)e * p.H * p.I) + wat + b0 * kBlk;
+    const float* ws = (sh ? p.ss2 : p.s2 + (int64_t)e * hb * ib) + sat + b0;
+    const uint8_t* h = p.hq + (int64_t)(u * 8 + g) * p.I + b0 * kBlk + 16 * t;
+    const float* hs = p.hs + (int64_t)(u * 8 + 2 * t) * ib + b0;
+    uint4 wv[kRun][4], hv[kRun][2];
+    float s[kRun][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) wv[j] = ldg_stream(w + (int64_t)8 * (j >> 1) * p.I + 64 * (j & 1));
+    for (int k = 0; k < kRun; ++k) {
+      const bool in = b0 + k < ib;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int tok = 8 * i + g, c0 = 8 * i + 2 * t, c1 = c0 + 1;
-      // a token that did not choose the expert has no h: its column is zero
-      // and takes nothing (not even a NaN of the weights)
-      x[0] = x[1] = make_uint4(0, 0, 0, 0);
-      if ((mask >> tok) & 1u) {
-        const uint8_t* h = p.hq + (int64_t)(u * p.T + tok) * p.I + b * kBlk + 16 * t;
-        x[0] = *reinterpret_cast<const uint4*>(h);
-        x[1] = *reinterpret_cast<const uint4*>(h + 64);
+      for (int j = 0; j < 4; ++j)
+        wv[k][j] = in ? ldg_stream(w + (int64_t)8 * (j >> 1) * p.I + 64 * (j & 1) + k * kBlk) : make_uint4(0, 0, 0, 0);
+      // a column without a token has no h: it is zero and adds nothing (not
+      // even a NaN of the weights)
+      hv[k][0] = hv[k][1] = make_uint4(0, 0, 0, 0);
+      if (in && ((cols >> g) & 1u)) {
+        hv[k][0] = *reinterpret_cast<const uint4*>(h + k * kBlk);
+        hv[k][1] = *reinterpret_cast<const uint4*>(h + k * kBlk + 64);
       }
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_block(d, wv, x);
-      if ((mask >> c0) & 1u) {
-        const float s = rw[u][c0] * (sw * p.hs[(int64_t)(u * p.T + c0) * ib + b]);
-        acc[i][0] = fmaf(s, d[0], acc[i][0]);
-        acc[i][2] = fmaf(s, d[2], acc[i][2]);
-      }
-      if ((mask >> c1) & 1u) {
-        const float s = rw[u][c1] * (sw * p.hs[(int64_t)(u * p.T + c1) * ib + b]);
-        acc[i][1] = fmaf(s, d[1], acc[i][1]);
-        acc[i][3] = fmaf(s, d[3], acc[i][3]);
-      }
+      const float sw = in ? ws[k] : 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) s[k][c] = in && ((cols >> (2 * t + c)) & 1u) ? sw * hs[c * ib + k] : 0.f;
     }
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_block(d, wv[k], hv[k]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = fmaf(s[k][j & 1], d[j], sum[j]);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if ((cols >> (2 * t + c)) & 1u) {
+        const float f = rw[u][2 * t + c];
+        if constexpr (GATHER) {  // a column's (row, token) is this lane's alone
+          const int tok = L.tok[u][2 * t + c];
+          sums[warp][g][tok] = fmaf(f, sum[c], sums[warp][g][tok]);
+          sums[warp][g + 8][tok] = fmaf(f, sum[c + 2], sums[warp][g + 8][tok]);
+        } else {
+          acc[c] = fmaf(f, sum[c], acc[c]);
+          acc[c + 2] = fmaf(f, sum[c + 2], acc[c + 2]);
+        }
+      }
+    if constexpr (GATHER) __syncwarp();  // the next run may bring the token in another column
   }
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[warp][4 * i + j][lane] = acc[i][j];
+  if constexpr (!GATHER) {
+    sums[warp][g][2 * t] = acc[0], sums[warp][g][2 * t + 1] = acc[1];
+    sums[warp][g + 8][2 * t] = acc[2], sums[warp][g + 8][2 * t + 1] = acc[3];
+  }
   __syncthreads();
-  for (int o = threadIdx.x; o < 128 * NT; o += 32 * kDnWarps) {
-    const int tok = o >> 4, r = o & 15, i = tok >> 3, c = tok & 7;
-    const int l = 4 * (r & 7) + (c >> 1), j = 4 * i + 2 * (r >> 3) + (c & 1);
+  for (int o = threadIdx.x; o < 16 * p.T; o += 32 * kDnWarps) {
+    const int tok = o >> 4, r = o & 15;
     float v = 0.f;
 #pragma unroll
-    for (int wq = 0; wq < kDnWarps; ++wq) v += part[wq][j][l];
-    if (tok < p.T) p.out[(int64_t)tok * p.H + n0 + r] = f32_to_bf16_rn(v);
+    for (int wq = 0; wq < kDnWarps; ++wq) v += sums[wq][r][tok];
+    p.out[(int64_t)tok * p.H + n0 + r] = f32_to_bf16_rn(v);
   }
 }
 
-int64_t list_cap(const fp4moe_dims& d) { return std::min(d.E, d.T * d.top_k) + d.n_shared; }
-
-int64_t hq_bytes(const fp4moe_dims& d) { return (list_cap(d) * d.T * d.I + 255) / 256 * 256; }
-
-template <int NT>
-cudaError_t launch(const ExpertsParams& p, int64_t cap, int sms, cudaStream_t s) {
-  const int64_t units = cap * (p.I / kBlk);
-  cudaError_t e = launch_pdl(experts_gateup_kernel<NT>, dim3((unsigned)std::min<int64_t>(units, 2 * sms)),
-                             dim3(kGuThreads), 0, s, p);
-  if (e == cudaSuccess) e = launch_pdl(experts_down_kernel<NT>, dim3(p.H / 16), dim3(32 * kDnWarps), 0, s, p);
-  return e;
+// Entries of the list: an expert with c tokens has ceil(c / 8) <= 1 + c / 8.
+int64_t list_cap(const fp4moe_dims& d) {
+  const int routes = d.T * d.top_k;
+  return std::min(d.E, routes) + (d.T > 8 ? routes / 8 : 0) + d.n_shared * ((d.T + 7) / 8);
 }
+
+int64_t hq_bytes(const fp4moe_dims& d) { return list_cap(d) * 8 * d.I; }  // a multiple of 1024
 
 }  // namespace
 
 size_t experts_fp8_workspace(const fp4moe_dims& d) {
-  return (size_t)(hq_bytes(d) + list_cap(d) * d.T * (d.I / kBlk) * 4);
+  return (size_t)(hq_bytes(d) + list_cap(d) * 8 * (d.I / kBlk) * 4);
 }
 
 cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weights& w, const uint8_t* xq,
@@ -283,7 +331,13 @@ cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weig
   p.hq = static_cast<uint8_t*>(ws);
   p.hs = reinterpret_cast<float*>(p.hq + hq_bytes(d));
   p.T = d.T, p.H = d.H, p.I = d.I, p.E = d.E, p.k = d.top_k, p.shared = d.n_shared;
-  return d.T <= 8 ? launch<1>(p, list_cap(d), sms, s) : launch<2>(p, list_cap(d), sms, s);
+  // one CTA fills an SM's registers; its units follow each other
+  const int64_t units = list_cap(d) * (d.I / kBlk);
+  const cudaError_t e = launch_pdl(experts_gateup_kernel, dim3((unsigned)std::min<int64_t>(units, sms)), dim3(kGuThreads),
+                                   0, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(d.T <= 8 ? experts_down_kernel<false> : experts_down_kernel<true>, dim3(d.H / 16), dim3(32 * kDnWarps), 0,
+                    s, p);
 }
 
 }  // namespace fp4moe

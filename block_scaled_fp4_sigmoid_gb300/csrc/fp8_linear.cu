@@ -19,15 +19,12 @@ struct StreamParams {
 
 constexpr int kStreamWarps = 8;
 
-// Few tokens: a CTA owns 16 weight rows and 8 NT tokens; its warps take the
-// 128-column blocks in turn, each streaming weights straight from global
-// memory into mma.sync operands (every byte once, 16 per lane), and their sums
-// are joined in warp order.  HBM bound: 8 tokens, 7168 x 36864 weights run at
-// 5.9 TB/s with four CTAs an SM (64 registers a thread); where the row tiles
-// do not even cover the SMs, the latency of a warp's chain counts instead and
-// more registers (more loads in flight a warp) win: 8 x 7168 x 2112 4.3 us
-// against 5.3.
-template <int NT, int MIN_CTAS>
+// Few tokens: a CTA owns 16 weight rows and 8 NT tokens; its warps take runs of
+// RUN 128-column blocks in turn, all loads of a run issued together, straight
+// from global memory into mma.sync operands (every weight byte once, 16 per
+// lane), and their sums are joined in warp order.  HBM bound: 8 tokens and 7168
+// x 36864 weights in 44 us, 6.0 TB/s.
+template <int NT, int MIN_CTAS, int RUN>
 __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_kernel(const StreamParams p) {
   __shared__ float part[kStreamWarps][NT * 4][32];
   pdl_wait();
@@ -41,28 +38,41 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
   float acc[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  for (int b = warp; b < nb; b += kStreamWarps) {
-    uint4 w[4];
-    const int k0 = b * kBlk;
-    const bool in[2] = {k0 + 16 * t < p.K, k0 + 16 * t + 64 < p.K};
+#pragma unroll 1
+  for (int b0 = warp * RUN; b0 < nb; b0 += kStreamWarps * RUN) {
+    uint4 w[RUN][4];
+    float sw[RUN];
+    bool in[RUN][2];
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = in[j & 1] ? ldg_stream((j < 2 ? w0 : w1) + k0 + 64 * (j & 1)) : zero;
-    const float sw = ws[b];
+    for (int r = 0; r < RUN; ++r) {
+      const int k0 = (b0 + r) * kBlk;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) in[r][j] = k0 + 16 * t + 64 * j < p.K;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[r][j] = in[r][j & 1] ? ldg_stream((j < 2 ? w0 : w1) + k0 + 64 * (j & 1)) : zero;
+      sw[r] = ws[min(b0 + r, nb - 1)];
+    }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const uint8_t* xr = p.xq + (int64_t)min(8 * i + g, p.T - 1) * p.K + k0 + 16 * t;
-      uint4 x[2];
+      const uint8_t* xr = p.xq + (int64_t)min(8 * i + g, p.T - 1) * p.K + b0 * kBlk + 16 * t;
+      const float* xs0 = p.xs + (int64_t)min(8 * i + 2 * t, p.T - 1) * nb;
+      const float* xs1 = p.xs + (int64_t)min(8 * i + 2 * t + 1, p.T - 1) * nb;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[j] = in[j] ? *reinterpret_cast<const uint4*>(xr + 64 * j) : zero;
-      const float s0 = sw * p.xs[(int64_t)min(8 * i + 2 * t, p.T - 1) * nb + b];
-      const float s1 = sw * p.xs[(int64_t)min(8 * i + 2 * t + 1, p.T - 1) * nb + b];
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_block(d, w, x);
-      acc[i][0] = fmaf(s0, d[0], acc[i][0]);
-      acc[i][1] = fmaf(s1, d[1], acc[i][1]);
-      acc[i][2] = fmaf(s0, d[2], acc[i][2]);
-      acc[i][3] = fmaf(s1, d[3], acc[i][3]);
+      for (int r = 0; r < RUN; ++r) {
+        uint4 x[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) x[j] = in[r][j] ? *reinterpret_cast<const uint4*>(xr + r * kBlk + 64 * j) : zero;
+        const int b = min(b0 + r, nb - 1);
+        // (a block past the end: its product is exactly zero, whatever the scales are not NaN)
+        const float s0 = b0 + r < nb ? sw[r] * xs0[b] : 0.f, s1 = b0 + r < nb ? sw[r] * xs1[b] : 0.f;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_block(d, w[r], x);
+        acc[i][0] = fmaf(s0, d[0], acc[i][0]);
+        acc[i][1] = fmaf(s1, d[1], acc[i][1]);
+        acc[i][2] = fmaf(s0, d[2], acc[i][2]);
+        acc[i][3] = fmaf(s1, d[3], acc[i][3]);
+      }
     }
   }
 #pragma unroll
@@ -93,17 +103,30 @@ constexpr int kStreamMaxT = 16;
 
 size_t linear_fp8_workspace(int, int, int) { return 256; }
 
-// Up to 16 tokens are streamed (measured at 7168 x 7168: 16 tokens 15-17 us
-// against 20 us of the tensor-core kernel; at 32 tokens 37 us against 16 us).
+// Up to 16 tokens are streamed (measured at 7168 x 7168: 16 tokens 13 us against
+// 20 us of the tensor-core kernel; 32 tokens 37 us against 16 us).
+//
+// The more CTAs share an SM, the fewer registers and so the fewer loads in
+// flight a warp.  With more row tiles than that, two blocks a run and three CTAs
+// an SM stream best, unless the last round of CTAs would be much emptier than
+// with one block and four CTAs (7168 x 7168, 448 tiles, 8 tokens: 11.0 us against
+// 11.9; 7168 x 36864, 2304 tiles: 49.6 against 43.9).  Where the tiles hardly
+// cover the SMs, four blocks a run (7168 x 2112, 132 tiles: 4.4 us against 5.2;
+// 16 tokens 6.9 against 10.1).
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
   if (a.T > kStreamMaxT) return launch_linear_fp8_tc(a, s);
   const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
                        a.out_fp32 ? 1 : 0};
-  const unsigned rows = (unsigned)((a.N + 15) / 16);
-  const dim3 grid(rows), block(32 * kStreamWarps);
-  if (a.T > 8) return launch_pdl(linear_stream_kernel<2, 1>, grid, block, 0, s, p);
-  if (rows <= 152) return launch_pdl(linear_stream_kernel<1, 1>, grid, block, 0, s, p);
-  return launch_pdl(linear_stream_kernel<1, 4>, grid, block, 0, s, p);
+  const int64_t tiles = (a.N + 15) / 16, sms = 152;
+  const dim3 grid((unsigned)tiles), block(32 * kStreamWarps);
+  if (a.T > 8) {
+    if (tiles <= sms) return launch_pdl(linear_stream_kernel<2, 1, 4>, grid, block, 0, s, p);
+    return launch_pdl(linear_stream_kernel<2, 3, 2>, grid, block, 0, s, p);
+  }
+  if (tiles <= 2 * sms) return launch_pdl(linear_stream_kernel<1, 2, 4>, grid, block, 0, s, p);
+  const int64_t at3 = (tiles + 3 * sms - 1) / (3 * sms) * 3, at4 = (tiles + 4 * sms - 1) / (4 * sms) * 4;  // CTA slots
+  if (at3 <= at4) return launch_pdl(linear_stream_kernel<1, 3, 2>, grid, block, 0, s, p);
+  return launch_pdl(linear_stream_kernel<1, 4, 1>, grid, block, 0, s, p);
 }
 
 }  // namespace fp4moe

@@ -82,8 +82,9 @@ def test_experts_arguments_and_workspace(lib):
     assert experts(lib, fm.make_dims(16, 320, 128, 8, 2, fmt=fm.FP8), full) == SHAPE
     shared = fm.make_dims(16, 256, 128, 8, 2, n_shared=1, fmt=fm.FP8)
     assert experts(lib, shared, fm.Fp8BlockWeights(P, P, P, P)) == INVALID
-    # the requantised h of every chosen expert and token fits
-    for T, E, k, sh in ((1, 8, 1, 0), (16, 8, 2, 1), (16, 512, 16, 1)):
+    # the requantised h of every route (and of the shared expert) fits, in rows of eight tokens
+    for T, E, k, sh in ((1, 8, 1, 0), (16, 8, 2, 1), (16, 512, 16, 1), (16, 16, 16, 0)):
         n = fm.experts_fp8_block_workspace_size(fm.make_dims(T, 256, 128, E, k, n_shared=sh, fmt=fm.FP8))
-        assert n >= (min(E, T * k) + sh) * T * (128 + 4)
+        entries = T * k if E >= T * k else max(E, -(-T * k // 8))
+        assert n >= 8 * (entries + sh * -(-T // 8)) * (128 + 4)
     assert lib.fp4moe_experts_fp8_block_workspace_size(ctypes.byref(fm.make_dims(17, 256, 128, 8, 2, fmt=fm.FP8))) == 0
