@@ -2,8 +2,8 @@
 // each with E4M3 codes and one fp32 scale per 128 columns.
 //
 // Both read their inputs once and write their outputs once (HBM bound): a
-// thread holds 8 consecutive columns (one 16-byte bf16 load), 16 lanes one
-// scale block, whose largest magnitude is a 16-lane shuffle reduction.
+// thread loads 8 consecutive columns at a time (16 bytes of bf16), 16 or 8 lanes
+// share a scale block, whose largest magnitude is a shuffle reduction.
 #include <algorithm>
 
 #include "fp8_block.cuh"
@@ -32,27 +32,30 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
 }
 
+// Codes of 8 values over a scale s with reciprocal r.
+__device__ __forceinline__ void store_codes(const float* v, float s, float r, uint8_t* q) {
+  float t[8];
+  if (s >= 1.17549435e-38f) {  // (one test for the eight)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = v[j] * r;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = e4m3_scaled(v[j], s, r);
+  }
+  *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]));
+}
+
 // Codes and scale of the 16-lane group's block from each lane's 8 values; all
 // 16 lanes take part (v = 0 past the row's end).
 __device__ __forceinline__ void quant_block(const float* v, bool in, uint8_t* q, float* scale) {
-  const uint32_t half = 0xffffu << ((threadIdx.y * blockDim.x + threadIdx.x) & 16);
   float amax = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[j]));
 #pragma unroll
-  for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(half, amax, o));
+  for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), amax, o));
   const float s = e4m3_scale(amax);
   if (in) {
-    const float r = __fdiv_rn(1.f, s);
-    float t[8];
-    if (s >= 1.17549435e-38f) {  // (one test for the eight)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = v[j] * r;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = e4m3_scaled(v[j], s, r);
-    }
-    *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]));
+    store_codes(v, s, __fdiv_rn(1.f, s), q);
     if ((threadIdx.x & 15) == 0) *scale = s;
   }
 }
@@ -127,29 +130,43 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams p) {
   }
 }
 
-// Thread per 8 columns of h.  Blocks are blockDim.x threads along a row (whole
-// 16-lane groups) by blockDim.y rows, so that no index is divided: with a flat
-// index its 64-bit division was a third of the instructions.
+// Eight lanes a scale block: lane l takes columns 8 l .. and 64 + 8 l .. of it.
+// Blocks are blockDim.x threads along a row by blockDim.y rows, so that no
+// index is divided.  Issue slots ran out before the memory did (81% of them at
+// 4096 x 18432 with 16 lanes of 8 columns, 67 us; with a flat index, divided
+// by the row's length, 69 us), so the block's reduction and its two divisions
+// are shared by 16 columns a lane.
 __global__ void __launch_bounds__(256) swiglu_fp8_kernel(const uint16_t* gu, int64_t gu_ld, int T, int I, uint8_t* q,
                                                          float* scales) {
   pdl_wait();
   pdl_trigger();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int c = blockIdx.y * blockDim.x + threadIdx.x;
-  if (row >= T || c >= 16 * blocks128(I)) return;  // whole groups
-  const bool in = 8 * c < I;
-  float h[8];
+  const int l = threadIdx.x & 7, b = blockIdx.y * (blockDim.x >> 3) + (threadIdx.x >> 3), nb = blocks128(I);
+  if (row >= T || b >= nb) return;  // whole groups of lanes
+  const int c0 = b * kBlk + 8 * l;
+  const uint16_t* src = gu + row * gu_ld + c0;
+  float h[2][8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = 0.f;
-  if (in) {
+  for (int k = 0; k < 2; ++k) {
+    uint4 gw = make_uint4(0, 0, 0, 0), uw = gw;
+    if (c0 + 64 * k < I) gw = ldg_stream(src + 64 * k), uw = ldg_stream(src + I + 64 * k);
     float g[8], u[8];
-    const uint16_t* src = gu + row * gu_ld + 8 * c;
-    unpack8(ldg_stream(src), g);
-    unpack8(ldg_stream(src + I), u);
+    unpack8(gw, g);
+    unpack8(uw, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = swiglu(g[j], u[j]);
+    for (int j = 0; j < 8; ++j) h[k][j] = swiglu(g[j], u[j]);
   }
-  quant_block(h, in, q + row * I + 8 * c, scales + row * blocks128(I) + (c >> 4));
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = max_nan(amax, fabsf(h[j >> 3][j & 7]));
+  const uint32_t lanes = 0xffu << ((threadIdx.y * blockDim.x + threadIdx.x) & 24);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(lanes, amax, o));
+  const float s = e4m3_scale(amax), r = __fdiv_rn(1.f, s);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (c0 + 64 * k < I) store_codes(h[k], s, r, q + row * I + c0 + 64 * k);
+  if (l == 0) scales[row * nb + b] = s;
 }
 
 }  // namespace
@@ -174,8 +191,8 @@ cudaError_t launch_add_rmsnorm(const uint16_t* x, int64_t x_ld, const uint16_t* 
 
 cudaError_t launch_swiglu_fp8(const uint16_t* gu, int64_t gu_ld, int T, int I, uint8_t* q, float* scales,
                               cudaStream_t s) {
-  const int groups = blocks128(I), bx = 16 * std::min(groups, 16), by = 256 / bx;
-  const dim3 grid((unsigned)((T + by - 1) / by), (unsigned)((16 * groups + bx - 1) / bx));
+  const int nb = blocks128(I), bx = 8 * std::min(nb, 32), by = 256 / bx;
+  const dim3 grid((unsigned)((T + by - 1) / by), (unsigned)((8 * nb + bx - 1) / bx));
   return launch_pdl(swiglu_fp8_kernel, grid, dim3(bx, by), 0, s, gu, gu_ld, T, I, q, scales);
 }
 

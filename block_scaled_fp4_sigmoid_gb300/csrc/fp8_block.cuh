@@ -66,8 +66,13 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return r;
 }
 
-// silu(g) * u with the hardware exponential and reciprocal.
-__device__ __forceinline__ float swiglu(float g, float u) { return g * rcp_approx(1.f + __expf(-g)) * u; }
+// silu(g) * u with the hardware base-2 exponential (results below the normal
+// range flush to zero: 1 + e^-g is 1 then) and reciprocal.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+  return g * rcp_approx(1.f + e) * u;
+}
 
 // d += A (16 x 32) . B (32 x 8), E4M3 inputs, fp32 accumulation.  With lane =
 // 4 g + t: a0, a2 from row g, a1, a3 from row g + 8, b0, b1 from column g;

@@ -2,7 +2,9 @@
 token and 128 columns (activations) or per 128 x 128 block (weights).
 
 The functions check their tensors, allocate what the caller does not pass and
-call the library on the current stream of the tensors' device.  Codes are
+call the library on the current stream of the tensors' device.  (Each check is
+one expression over all tensors, a few microseconds less than one call a
+tensor; what is wrong is worked out only once something is.)  Codes are
 torch.uint8 or torch.float8_e4m3fn tensors.  ``Fp8BlockMlp`` and
 ``Fp8BlockMoE`` run them together as the two feed-forward sublayers of a
 decoder layer.
@@ -17,7 +19,8 @@ from . import (FP8, Dims, Fp8BlockWeights, add_rmsnorm_fp8 as _add_rmsnorm, expe
 
 BLOCK = 128
 _CODES = (torch.uint8, torch.float8_e4m3fn)
-_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_bf16, _f32 = torch.bfloat16, torch.float32
+_BF16, _F32 = (_bf16,), (_f32,)
 _OUT = _BF16 + _F32
 
 
@@ -71,19 +74,30 @@ def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None
     want_y is set, else None is returned in its place."""
     if x.dim() != 2:
         raise ValueError(f"x: a matrix expected, got {tuple(x.shape)}")
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
     dev = _device(x)
-    _check("x", x, (T, H), _BF16, dev, dense=False)
-    _check("gamma", gamma, (H,), _BF16, dev)
-    if residual is not None:
-        _check("residual", residual, (T, H), _BF16, dev)
-        residual_out = _out("residual_out", residual_out, (T, H), _BF16, dev)
-    elif residual_out is not None:
-        _check("residual_out", residual_out, (T, H), _BF16, dev)
-    if y is not None or want_y:
-        y = _out("y", y, (T, H), _BF16, dev)
-    q = _out("q", q, (T, H), _CODES, dev)
-    scales = _out("scales", scales, (T, _blocks(H)), _F32, dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=_bf16, device=x.device)
+    if y is None and want_y:
+        y = torch.empty(shape, dtype=_bf16, device=x.device)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((T, (H + 127) // 128), dtype=_f32, device=x.device)
+    if not (x.dtype is _bf16 and (x.stride(1) == 1 or H == 1) and gamma.dtype is _bf16 and gamma.shape == (H,)
+            and gamma.is_contiguous() and q.dtype in _CODES and q.shape == shape and q.is_contiguous()
+            and scales.dtype is _f32 and scales.shape == (T, (H + 127) // 128) and scales.is_contiguous()
+            and gamma.get_device() == q.get_device() == scales.get_device() == dev
+            and all(t is None or t.dtype is _bf16 and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+                    for t in (residual, residual_out, y))):
+        _check("x", x, shape, _BF16, dev, dense=False)
+        _check("gamma", gamma, (H,), _BF16, dev)
+        for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
+            if t is not None:
+                _check(name, t, shape, _BF16, dev)
+        _check("q", q, shape, _CODES, dev)
+        _check("scales", scales, (T, _blocks(H)), _F32, dev)
     if T:
         _add_rmsnorm(x.data_ptr(), _ld(x), _ptr(residual), gamma.data_ptr(), T, H, eps, _ptr(residual_out), _ptr(y),
                      q.data_ptr(), scales.data_ptr(), _stream(dev))
@@ -95,11 +109,19 @@ def swiglu_fp8(gu, *, q=None, scales=None):
     may be strided."""
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError(f"gu: [T, 2I] expected, got {tuple(gu.shape)}")
-    T, I = gu.shape[0], gu.shape[1] // 2
+    T, I = gu.shape
+    I //= 2
     dev = _device(gu)
-    _check("gu", gu, (T, 2 * I), _BF16, dev, dense=False)
-    q = _out("q", q, (T, I), _CODES, dev)
-    scales = _out("scales", scales, (T, _blocks(I)), _F32, dev)
+    if q is None:
+        q = torch.empty((T, I), dtype=torch.uint8, device=gu.device)
+    if scales is None:
+        scales = torch.empty((T, (I + 127) // 128), dtype=_f32, device=gu.device)
+    if not (gu.dtype is _bf16 and gu.stride(1) == 1 and q.dtype in _CODES and q.shape == (T, I) and q.is_contiguous()
+            and scales.dtype is _f32 and scales.shape == (T, (I + 127) // 128) and scales.is_contiguous()
+            and q.get_device() == scales.get_device() == dev):
+        _check("gu", gu, (T, 2 * I), _BF16, dev, dense=False)
+        _check("q", q, (T, I), _CODES, dev)
+        _check("scales", scales, (T, _blocks(I)), _F32, dev)
     if T:
         _swiglu(gu.data_ptr(), _ld(gu), T, I, q.data_ptr(), scales.data_ptr(), _stream(dev))
     return q, scales
@@ -114,17 +136,25 @@ def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, 
     if xq.dim() != 2 or w.dim() != 2:
         raise ValueError(f"xq and w: matrices expected, got {tuple(xq.shape)} and {tuple(w.shape)}")
     (T, K), N = xq.shape, w.shape[0]
+    kb = (K + 127) // 128
     dev = _device(xq)
-    _check("xq", xq, (T, K), _CODES, dev)
-    _check("xs", xs, (T, _blocks(K)), _F32, dev)
-    _check("w", w, (N, K), _CODES, dev)
-    _check("w_scale", w_scale, (_blocks(N), _blocks(K)), _F32, dev)
-    if out_dtype not in _OUT:
-        raise ValueError(f"out_dtype: bf16 or fp32, got {out_dtype}")
-    out = _out("out", out, (T, N), (out_dtype,) if out is None else _OUT, dev, dense=False)
+    if out is None:
+        if out_dtype not in _OUT:
+            raise ValueError(f"out_dtype: bf16 or fp32, got {out_dtype}")
+        out = torch.empty((T, N), dtype=out_dtype, device=xq.device)
+    if not (xq.dtype in _CODES and xq.is_contiguous() and xs.dtype is _f32 and xs.shape == (T, kb) and xs.is_contiguous()
+            and w.dtype in _CODES and w.shape[1] == K and w.is_contiguous() and w_scale.dtype is _f32
+            and w_scale.shape == ((N + 127) // 128, kb) and w_scale.is_contiguous() and out.dtype in _OUT
+            and out.shape == (T, N) and (out.stride(1) == 1 or N == 1)
+            and xs.get_device() == w.get_device() == w_scale.get_device() == out.get_device() == dev):
+        _check("xq", xq, (T, K), _CODES, dev)
+        _check("xs", xs, (T, kb), _F32, dev)
+        _check("w", w, (N, K), _CODES, dev)
+        _check("w_scale", w_scale, (_blocks(N), kb), _F32, dev)
+        _check("out", out, (T, N), _OUT, dev, dense=False)
     if T:
         _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), _ld(out),
-                out.dtype == torch.float32, _ptr(ws), ws.numel() if ws is not None else 0, _stream(dev))
+                out.dtype is _f32, _ptr(ws), ws.numel() if ws is not None else 0, _stream(dev))
     return out
 
 

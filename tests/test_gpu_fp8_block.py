@@ -348,6 +348,45 @@ def test_experts_on_another_stream_after_the_router(ops):
     assert torch.equal(mlp_out, ops.linear_fp8_block(hq, hs, sd[2], sd[3])) and torch.equal(mlp_res, mr)
 
 
+@pytest.mark.parametrize("T,H,I", [(6, 1024, 640), (130, 1024, 3584), (1024, 1024, 3584), (700, 2816, 256)])
+def test_calls_in_a_row_equal_calls_that_wait(ops, T, H, I):
+    """Each kernel starts while the one before it ends: a chain of calls that nothing waits
+    between, on rotating buffers, gives what the same calls give one by one (streamed, tiled,
+    split over clusters, and two launches a product)."""
+    import torch
+    rng = np.random.default_rng(T)
+    w13, s13 = dev(codes(rng, 2 * I, H)), dev((2e-4 * (0.5 + rng.random((2 * I // 128, B.blocks(H))))).astype(np.float32))
+    w2, s2 = dev(codes(rng, H, I)), dev((2e-4 * (0.5 + rng.random((B.blocks(H), B.blocks(I))))).astype(np.float32))
+    gamma = bf16(np.ones(H))[0]
+    xs = [bf16(rng.standard_normal((T, H)))[0] for _ in range(3)]
+
+    def step(x, res, sync):
+        out = []
+        res, _, q, s = ops.add_rmsnorm_fp8(x, res, gamma, 1e-6)
+        for f in (lambda: ops.linear_fp8_block(q, s, w13, s13), lambda: ops.swiglu_fp8(out[0]),
+                  lambda: ops.linear_fp8_block(*out[1], w2, s2)):
+            if sync:
+                torch.cuda.synchronize()
+            out.append(f())
+        return out[2], res
+
+    def run(sync):
+        seen = []
+        for x in xs:
+            y, res = x, x
+            for _ in range(6):
+                y, res = step(y, res, sync)
+                seen.append(y)
+        torch.cuda.synchronize()
+        return seen
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+    assert fm.linear_fp8_block_status() == (0, 0)
+
+
 def test_refusals_on_tensors(ops):
     import torch
     x = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
