@@ -128,6 +128,53 @@ __device__ __forceinline__ void tile_at(int tile, int mtiles, int ntiles, int& m
   mt = g * kGroupM + in - nt * gm;
 }
 
+// One warp's 32 staged rows (128 bytes each, 16-byte pieces xor-swizzled by the
+// row) to columns [col, col + cols) of rows row.. of out, where these are inside
+// it: whole aligned 16-byte vectors, eight lanes a row, and element by element
+// what sticks out of them at either end (a row of an odd width starts anywhere;
+// with elements alone 3228 x 2304 x 10881 took 147 us).
+__device__ __forceinline__ void store_rows(const TcParams& p, const uint8_t* stg, int lane, int row, int col, int cols) {
+  const int esz = p.out_fp32 ? 4 : 2, nbytes = min(cols, p.N - col) * esz, nrow = min(32, p.T - row);
+  if (nbytes <= 0) return;
+  uint8_t* dst = p.out + ((int64_t)row * p.out_ld + col) * esz;
+  const int64_t ld = p.out_ld * esz;
+  if (p.vec && nbytes == 128) {
+    uint8_t* d = dst + (lane >> 3) * ld + 16 * (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = (lane >> 3) + 4 * i;
+      const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      if (r < nrow) *reinterpret_cast<uint4*>(d + 4 * i * ld) = w;
+    }
+    return;
+  }
+  auto at = [&](int r, int byte) { return stg + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15); };
+#pragma unroll 1
+  for (int r = lane >> 3; r < nrow; r += 4) {
+    uint8_t* d = dst + r * ld;
+    const int l = lane & 7, off = (int)(reinterpret_cast<uintptr_t>(d) & 15u);  // of the row in its first vector
+    const int head = off ? min(16 - off, nbytes) : 0, tail = max(head, ((off + nbytes) & ~15) - off);
+    const int byte = head + 16 * l;  // where this lane's vector starts
+    if (byte < tail) {
+      uint32_t w[5];  // the five words that hold it
+#pragma unroll
+      for (int k = 0; k < 5; ++k)
+        w[k] = k < 4 || (byte & 2) ? *reinterpret_cast<const uint32_t*>(at(r, (byte & ~3) + 4 * k)) : 0u;
+      const uint32_t sh = (byte & 2) * 8;
+      *reinterpret_cast<uint4*>(d + byte) = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                                                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+    }
+    auto one = [&](int byte) {
+      if (p.out_fp32)
+        *reinterpret_cast<uint32_t*>(d + byte) = *reinterpret_cast<const uint32_t*>(at(r, byte));
+      else
+        *reinterpret_cast<uint16_t*>(d + byte) = *reinterpret_cast<const uint16_t*>(at(r, byte));
+    };
+    if (l * esz < head) one(l * esz);
+    if (tail + l * esz < nbytes) one(tail + l * esz);
+  }
+}
+
 template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const __grid_constant__ TcParams p) {
   using C = TcCfg<BN>;
@@ -313,7 +360,7 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
       if (tile + step < tiles) open_tile(tile + step);
       // through shared memory (16-byte pieces xor-swizzled by the row), so
       // that a store covers whole 128-byte runs of a row
-      const int esz = p.out_fp32 ? 4 : 2, per = 128 / esz;
+      const int per = p.out_fp32 ? 32 : 64;
 #pragma unroll
       for (int o = 0; o < C::kCols / 32; ++o) {  // 32 fp32 columns at a time; bf16 takes 64
         if (!p.out_fp32 && o >= C::kCols / 64) break;
@@ -335,29 +382,7 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
           *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
-        const int ncol = min(per, p.N - nc), nrow = min(32, p.T - st0);
-        uint8_t* dst = p.out + ((int64_t)st0 * p.out_ld + nc) * esz;
-        if (p.vec && ncol == per) {
-          uint8_t* d = dst + (int64_t)(lane >> 3) * p.out_ld * esz + 16 * (lane & 7);
-          const int64_t ld4 = 4 * p.out_ld * esz;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (lane >> 3) + 4 * i;
-            const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-            if (r < nrow) *reinterpret_cast<uint4*>(d + i * ld4) = w;
-          }
-        } else {
-          for (int r = 0; r < nrow; ++r)
-            for (int c = lane; c < ncol; c += 32) {
-              const int at = r * 128 + ((((c * esz) >> 4) ^ (r & 7)) << 4) + ((c * esz) & 15);
-              if (p.out_fp32)
-                *reinterpret_cast<uint32_t*>(dst + ((int64_t)r * p.out_ld + c) * 4) =
-                    *reinterpret_cast<const uint32_t*>(stg + at);
-              else
-                *reinterpret_cast<uint16_t*>(dst + ((int64_t)r * p.out_ld + c) * 2) =
-                    *reinterpret_cast<const uint16_t*>(stg + at);
-            }
-        }
+        store_rows(p, stg, lane, st0, nc, per);
         __syncwarp();
       }
     }
