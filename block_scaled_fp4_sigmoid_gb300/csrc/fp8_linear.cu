@@ -1,6 +1,8 @@
 // Block-scaled FP8 linear: out[t, n] = sum_b xs[t, b] ws[n / 128, b] *
 // sum_{k in block b} xq[t, k] w[n, k], E4M3 values, fp32 sums, bf16 or fp32 out.
 
+#include <algorithm>
+
 #include "fp8_block.cuh"
 #include "internal.h"
 
@@ -19,7 +21,7 @@ struct StreamParams {
 
 constexpr int kStreamWarps = 8;
 
-// Few tokens: a CTA owns 16 weight rows and 8 NT tokens; its warps take runs of
+// A CTA owns 16 weight rows and 8 NT tokens; its warps take runs of
 // RUN 128-column blocks in turn, all loads of a run issued together, straight
 // from global memory into mma.sync operands (every weight byte once, 16 per
 // lane), and their sums are joined in warp order.  HBM bound: 8 tokens and 7168
@@ -29,9 +31,9 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
   __shared__ float part[kStreamWarps][NT * 4][32];
   pdl_wait();
   pdl_trigger();
-  if (p.status && blockIdx.x == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
+  if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16, nb = blocks128(p.K);
+  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (8 * NT), nb = blocks128(p.K);
   const float* ws = p.ws + (int64_t)(n0 / kBlk) * nb;
   const uint8_t* w0 = p.w + (int64_t)min(n0 + g, p.N - 1) * p.K + 16 * t;  // past N: not stored
   const uint8_t* w1 = p.w + (int64_t)min(n0 + g + 8, p.N - 1) * p.K + 16 * t;
@@ -55,9 +57,9 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const uint8_t* xr = p.xq + (int64_t)min(8 * i + g, p.T - 1) * p.K + b0 * kBlk + 16 * t;
-      const float* xs0 = p.xs + (int64_t)min(8 * i + 2 * t, p.T - 1) * nb;
-      const float* xs1 = p.xs + (int64_t)min(8 * i + 2 * t + 1, p.T - 1) * nb;
+      const uint8_t* xr = p.xq + (int64_t)min(t0 + 8 * i + g, p.T - 1) * p.K + b0 * kBlk + 16 * t;
+      const float* xs0 = p.xs + (int64_t)min(t0 + 8 * i + 2 * t, p.T - 1) * nb;
+      const float* xs1 = p.xs + (int64_t)min(t0 + 8 * i + 2 * t + 1, p.T - 1) * nb;
 #pragma unroll
       for (int r = 0; r < RUN; ++r) {
         uint4 x[2];
@@ -87,8 +89,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
     float v = 0.f;
 #pragma unroll
     for (int wq = 0; wq < kStreamWarps; ++wq) v += part[wq][j][l];
-    if (tok < p.T && n0 + r < p.N) {
-      const int64_t at = (int64_t)tok * p.out_ld + n0 + r;
+    if (t0 + tok < p.T && n0 + r < p.N) {
+      const int64_t at = (int64_t)(t0 + tok) * p.out_ld + n0 + r;
       if (p.out_fp32)
         static_cast<float*>(p.out)[at] = v;
       else
@@ -97,14 +99,17 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
   }
 }
 
-constexpr int kStreamMaxT = 16;
-
 }  // namespace
 
 size_t linear_fp8_workspace(int, int, int) { return 256; }
 
 // Up to 16 tokens are streamed (measured at 7168 x 7168: 16 tokens 13 us against
-// 20 us of the tensor-core kernel; 32 tokens 37 us against 16 us).
+// 20 us of the tensor-core kernel; 32 tokens 37 us against 16 us).  From 17 to
+// 128 the weights would be streamed once for every 16 tokens, which small
+// products still do sooner than the tensor-core kernel starts and joins its
+// parts (64 x 2048 x 512: 2.8 us against 7.4, 32 x 7168 x 576 5.1 against 8.8; but
+// 32 x 7168 x 2112 12.4 against 9.9): the smaller of two estimates, both fitted to
+// such measurements, decides.
 //
 // The more CTAs share an SM, the fewer registers and so the fewer loads in
 // flight a warp.  With more row tiles than that, two blocks a run and three CTAs
@@ -114,17 +119,24 @@ size_t linear_fp8_workspace(int, int, int) { return 256; }
 // cover the SMs, four blocks a run (7168 x 2112, 132 tiles: 4.4 us against 5.2;
 // 16 tokens 6.9 against 10.1).
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
-  if (a.T > kStreamMaxT) return launch_linear_fp8_tc(a, s);
+  const int64_t rows = (a.N + 15) / 16, sms = 152, nb = blocks128(a.K);
+  const int64_t chunks = a.T > 8 ? (a.T + 15) / 16 : 1, ctas = rows * chunks;
+  if (a.T > 16) {
+    // in 10 ns; the launches differ by about 1 us
+    const int64_t stream = ctas <= sms ? nb * 52 / 10
+                                       : std::max((ctas + 3 * sms - 1) / (3 * sms) * nb * 35 / 2,
+                                                  chunks * a.N * (int64_t)a.K / 40000);  // (weights at 4 TB/s)
+    if (a.T > 128 || stream > linear_fp8_tc_cost(a.T, a.K, a.N) + 100) return launch_linear_fp8_tc(a, s);
+  }
   const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
                        a.out_fp32 ? 1 : 0};
-  const int64_t tiles = (a.N + 15) / 16, sms = 152;
-  const dim3 grid((unsigned)tiles), block(32 * kStreamWarps);
+  const dim3 grid((unsigned)rows, (unsigned)chunks), block(32 * kStreamWarps);
   if (a.T > 8) {
-    if (tiles <= sms) return launch_pdl(linear_stream_kernel<2, 1, 4>, grid, block, 0, s, p);
+    if (ctas <= sms) return launch_pdl(linear_stream_kernel<2, 1, 4>, grid, block, 0, s, p);
     return launch_pdl(linear_stream_kernel<2, 3, 2>, grid, block, 0, s, p);
   }
-  if (tiles <= 2 * sms) return launch_pdl(linear_stream_kernel<1, 2, 4>, grid, block, 0, s, p);
-  const int64_t at3 = (tiles + 3 * sms - 1) / (3 * sms) * 3, at4 = (tiles + 4 * sms - 1) / (4 * sms) * 4;  // CTA slots
+  if (ctas <= 2 * sms) return launch_pdl(linear_stream_kernel<1, 2, 4>, grid, block, 0, s, p);
+  const int64_t at3 = (ctas + 3 * sms - 1) / (3 * sms) * 3, at4 = (ctas + 4 * sms - 1) / (4 * sms) * 4;  // CTA slots
   if (at3 <= at4) return launch_pdl(linear_stream_kernel<1, 3, 2>, grid, block, 0, s, p);
   return launch_pdl(linear_stream_kernel<1, 4, 1>, grid, block, 0, s, p);
 }

@@ -1,12 +1,22 @@
 // Block-scaled FP8 linear for many tokens on the tensor cores (tcgen05,
 // E4M3 x E4M3, fp32 accumulators in tensor memory).
 //
-// The scales change every 128 columns of K and are arbitrary fp32 numbers,
-// so they cannot ride in the MMA: each K block's product goes to one of two
-// tensor-memory buffers, and the epilogue warps fold it, times xs[t, b]
-// ws[n / 128, b], into fp32 sums held in their registers while the MMAs of
-// the next block fill the other buffer.  Lanes are tokens, so a thread's
-// factor is one number per block: one fused multiply-add per element.
+// The scales change every 128 columns of K and are arbitrary fp32 numbers, so
+// they cannot ride in the MMA: each K block's product goes to a buffer of tensor
+// memory (two of 256 columns, four of 128), and the epilogue warps fold it,
+// times xs[t, b] ws[n / 128, b], into fp32 sums held in their registers while the
+// MMAs of the next blocks fill the other buffers.  Lanes are tokens, so a
+// thread's factor is one number a block: one fused multiply-add per element, two
+// to an instruction.
+//
+// What bounds it: shared memory.  A K block of a 128 x 256 tile writes 48 KB of
+// operands there and the MMAs read them again, 768 cycles at 128 bytes a cycle
+// against 512 of the tensor core (fp8); measured 780 without the epilogue's
+// sums, 840 with them (16384 x 7168 x 7168 in 593 us, 2.84 PFLOP/s).  Run for
+// seconds the board's power cap takes the clock to 1.6 GHz: 680 us.  CTA pairs
+// (256 x 256 over two SMs, 512 cycles of shared memory) reached 474 us without
+// the sums but 615 with them: two buffers of tensor memory are then too few for
+// the way round over both CTAs.  Operands multicast to two CTAs changed nothing.
 //
 // Work split: with about a tile or more for every SM, persistent CTAs take whole
 // tiles in turn, 256 weight rows wide where that fills whole rounds and 128
@@ -15,8 +25,8 @@
 // with a run of its K blocks; the sums meet in distributed shared memory,
 // where each CTA adds a slice of the columns over the runs, in the order of K.
 //
-// Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 4-11 epilogue
-// (a warp group of their own, with the larger register share).  Every wait
+// Warp roles: warp 0 TMA producer, warps 1 and 2 MMA issuers, warps 4-11 epilogue
+// (warp groups of their own, with the larger register share).  Every wait
 // is bounded; a timeout records FP4MOE_ERR_TIMEOUT in the status word, drains
 // copies and MMAs in flight, frees tensor memory and returns.
 #include <cuda.h>
@@ -56,7 +66,7 @@ struct TcParams {
 
 template <int BN>
 struct TcCfg {
-  static constexpr int kEpiWarps = 8, kThreads = 128 + 32 * kEpiWarps;  // warps 2 and 3 idle
+  static constexpr int kEpiWarps = 8, kThreads = 128 + 32 * kEpiWarps;  // warp 3 idles
   static constexpr int kCols = BN / 2;  // columns of one epilogue warp
   static constexpr int kABytes = 128 * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
   static constexpr int kStages = BN == 256 ? 4 : 6;
@@ -266,8 +276,9 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
     __syncwarp();
   } else if (warp < 3) {
     // ------------------------------------------------------------ MMA issuers
-    // Two, for the even and the odd K blocks: issuing a block's four MMAs and
-    // its two commits takes one warp longer than the tensor core needs for it.
+    // Two, for the even and the odd K blocks: issuing a block's four MMAs and its
+    // two commits takes one warp longer than the tensor core needs for it (128-wide
+    // tiles 968 -> 801 us at 16384 x 7168 x 7168).
     const uint64_t a0 = desc_sw128_k(sbase), b0 = desc_sw128_k(sbase + C::kABytes);
     int stage = warp - 1, buf = warp - 1;
     uint32_t phase = 0, bphase = 0;
@@ -507,24 +518,26 @@ cudaError_t launch_tc(const LinearFp8Args& a, int split, bool second, cudaStream
 // How a call is run: columns [0, wide) in tiles of 256, the rest in tiles of
 // 128; split > 1: all of it in tiles of 128 shared by `split` CTAs.  Chosen by
 // the time per K block of a tile (measured: 0.43 us 256 wide, 0.29 us 128
-// wide; joining a split tile 3 us) and the rounds that the tiles make on 152
-// SMs.  A split tile's CTAs are a cluster, and as many clusters as run at the
-// same time are taken (72 of 2, 32 of 4, 16 of 8: more would make a second
-// round, measured at twice the time).
+// wide; joining a split tile 3.5 us) and the rounds that the tiles make on 152
+// SMs.  A split tile's CTAs are a cluster, and no more clusters are taken than
+// run at the same time (measured: 15 of 8, 36 and more of 4, 76 of 2; a second
+// round doubles the time, 128 x 4096 x 1920 9.1 us, x 2048 15.9).
 struct TcChoice {
   int wide, split;
+  int64_t cost;  // in 10 ns, without the launch
 };
 TcChoice choose(int T, int K, int N) {
-  constexpr int64_t kT256 = 43, kT128 = 29, kJoin = 300;  // 10 ns
+  constexpr int64_t kT256 = 43, kT128 = 29, kJoin = 350;  // 10 ns
   const int64_t nb = blocks128(K), mt = (T + 127) / 128, sms = kTcCtas;
   const int64_t n128 = (N + 127) / 128;
-  TcChoice best{0, 1};
+  TcChoice best{0, 1, 0};
   int64_t cost = (mt * n128 + sms - 1) / sms * nb * kT128;
   for (int split = 2; split <= 8; split *= 2) {
     const int64_t c = (nb + split - 1) / split * kT128 + kJoin;
-    if (mt * n128 <= (split == 2 ? 72 : split == 4 ? 32 : 16) && nb >= 2 * split && c < cost) cost = c, best = {0, split};
+    if (mt * n128 <= (split == 2 ? 75 : split == 4 ? 36 : 14) && nb >= 2 * split && c < cost) cost = c, best = {0, split, 0};
   }
-  for (int64_t w = (N + 255) / 256; w > 0; --w) {  // w tiles of 256, the rest of 128
+  const int64_t all = (N + 255) / 256;
+  for (int64_t w = all; w > 0 && (all - w) * mt <= 2 * sms; --w) {  // w tiles of 256, the rest (two rounds at most) of 128
     const int64_t rest = std::max<int64_t>(0, n128 - 2 * w) * mt, t = w * mt, full = t / sms, late = t % sms;
     // the SMs with a tile less take the first of the rest
     const int64_t early = sms - late;
@@ -535,8 +548,9 @@ TcChoice choose(int T, int K, int N) {
       c += (more + sms - 1) / sms * kT128;
     }
     c = c * nb + (rest > 0 ? 100 : 0);  // 1 us for the second launch
-    if (c < cost) cost = c, best = {(int)std::min<int64_t>(256 * w, N), 1};
+    if (c < cost) cost = c, best = {(int)std::min<int64_t>(256 * w, N), 1, 0};
   }
+  best.cost = cost;
   return best;
 }
 
@@ -548,6 +562,8 @@ cudaError_t linear_fp8_status_word(int32_t** word) {
   *word = static_cast<int32_t*>(p);
   return e;
 }
+
+int64_t linear_fp8_tc_cost(int T, int K, int N) { return choose(T, K, N).cost; }
 
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s) {
   const TcChoice c = choose(a.T, a.K, a.N);

@@ -157,6 +157,7 @@ cudaError_t linear_fp8_status_word(int32_t** word);  // the current device's, of
 size_t linear_fp8_workspace(int T, int K, int N);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s);  // tensor cores
+int64_t linear_fp8_tc_cost(int T, int K, int N);  // its time in 10 ns, without the launch
 constexpr int kExpertsMaxT = 16;
 size_t experts_fp8_workspace(const fp4moe_dims& d);
 cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weights& w, const uint8_t* xq,

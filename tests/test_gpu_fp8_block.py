@@ -172,7 +172,7 @@ def linear_inputs(T, K, N, seed):
 
 SHAPES = [(1, 16, 1), (1, 7168, 576), (7, 256, 65), (8, 144, 128), (9, 1040, 130), (16, 2048, 272), (17, 512, 257),
           (31, 400, 100), (33, 1024, 513), (64, 2064, 64), (65, 128, 384), (128, 640, 256), (129, 1536, 1000),
-          (200, 272, 31), (300, 512, 768), (513, 896, 515), (1025, 384, 640), (40, 48, 130),
+          (200, 272, 31), (300, 512, 768), (513, 896, 515), (1025, 384, 640), (40, 48, 130), (150, 48, 130),
           (140, 2704, 300), (257, 2704, 1100), (513, 2704, 1200), (1024, 1024, 7168), (1030, 1040, 7101)]
 
 
