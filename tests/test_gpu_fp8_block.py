@@ -204,6 +204,22 @@ def test_linear_writes_its_columns_of_a_wider_output_only(ops, T, K, N):
     assert bool((wide == 7.0).all())
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("T,K,N", [(20, 256, 100), (300, 384, 523), (1030, 1040, 7100), (1024, 1024, 7168), (140, 2704, 300)])
+def test_linear_into_aligned_columns_of_a_wider_output(ops, T, K, N, fp32):
+    """As above with rows and first column on 16 bytes, where whole boxes are stored: their
+    parts outside [T, N] stay as they were."""
+    import torch
+    dtype = torch.float32 if fp32 else torch.bfloat16
+    a = [dev(v) for v in linear_inputs(T, K, N, 5)]
+    want = ops.linear_fp8_block(*a, out_dtype=dtype)
+    wide = torch.full((T + 33, (N + 90) // 8 * 8), 7.0, dtype=dtype, device="cuda")
+    ops.linear_fp8_block(*a, out=wide[:T, 8:8 + N])
+    assert torch.equal(wide[:T, 8:8 + N], want)
+    wide[:T, 8:8 + N] = 7.0
+    assert bool((wide == 7.0).all())
+
+
 @pytest.mark.parametrize("T,K,N", [(2, 256, 40), (40, 384, 300), (260, 512, 300)])
 def test_linear_nan_stays_in_its_row_and_column(ops, T, K, N):
     xq, xs, wq, ws = linear_inputs(T, K, N, 6)
