@@ -42,11 +42,6 @@ def _check(name, t, shape, dtypes, device, dense=True):
         raise ValueError(f"{name}: {'row-major' if dense else 'unit column stride'} expected, strides are {t.stride()}")
 
 
-def _ld(t):
-    """Row stride of a matrix in elements (one row: its length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
 def _out(name, t, shape, dtypes, device, dense=True):
     if t is None:
         return torch.empty(shape, dtype=dtypes[0], device=f"cuda:{device}")
@@ -89,8 +84,11 @@ def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None
             and gamma.is_contiguous() and q.dtype in _CODES and q.shape == shape and q.is_contiguous()
             and scales.dtype is _f32 and scales.shape == (T, (H + 127) // 128) and scales.is_contiguous()
             and gamma.get_device() == q.get_device() == scales.get_device() == dev
-            and all(t is None or t.dtype is _bf16 and t.shape == shape and t.is_contiguous() and t.get_device() == dev
-                    for t in (residual, residual_out, y))):
+            and (residual is None or residual.dtype is _bf16 and residual.shape == shape and residual.is_contiguous()
+                 and residual.get_device() == dev)
+            and (residual_out is None or residual_out.dtype is _bf16 and residual_out.shape == shape
+                 and residual_out.is_contiguous() and residual_out.get_device() == dev)
+            and (y is None or y.dtype is _bf16 and y.shape == shape and y.is_contiguous() and y.get_device() == dev)):
         _check("x", x, shape, _BF16, dev, dense=False)
         _check("gamma", gamma, (H,), _BF16, dev)
         for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
@@ -99,8 +97,9 @@ def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None
         _check("q", q, shape, _CODES, dev)
         _check("scales", scales, (T, _blocks(H)), _F32, dev)
     if T:
-        _add_rmsnorm(x.data_ptr(), _ld(x), _ptr(residual), gamma.data_ptr(), T, H, eps, _ptr(residual_out), _ptr(y),
-                     q.data_ptr(), scales.data_ptr(), _stream(dev))
+        _add_rmsnorm(x.data_ptr(), x.stride(0) if T > 1 else H, None if residual is None else residual.data_ptr(),
+                     gamma.data_ptr(), T, H, eps, None if residual_out is None else residual_out.data_ptr(),
+                     None if y is None else y.data_ptr(), q.data_ptr(), scales.data_ptr(), _stream(dev))
     return residual_out if residual_out is not None else x, y, q, scales
 
 
@@ -123,7 +122,7 @@ def swiglu_fp8(gu, *, q=None, scales=None):
         _check("q", q, (T, I), _CODES, dev)
         _check("scales", scales, (T, _blocks(I)), _F32, dev)
     if T:
-        _swiglu(gu.data_ptr(), _ld(gu), T, I, q.data_ptr(), scales.data_ptr(), _stream(dev))
+        _swiglu(gu.data_ptr(), gu.stride(0) if T > 1 else 2 * I, T, I, q.data_ptr(), scales.data_ptr(), _stream(dev))
     return q, scales
 
 
@@ -153,8 +152,9 @@ def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, 
         _check("w_scale", w_scale, (_blocks(N), kb), _F32, dev)
         _check("out", out, (T, N), _OUT, dev, dense=False)
     if T:
-        _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), _ld(out),
-                out.dtype is _f32, _ptr(ws), ws.numel() if ws is not None else 0, _stream(dev))
+        _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
+                out.stride(0) if T > 1 else N, out.dtype is _f32, None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel(), _stream(dev))
     return out
 
 
