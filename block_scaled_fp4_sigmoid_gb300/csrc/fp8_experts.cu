@@ -191,8 +191,6 @@ __global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const Exp
   }
 }
 
-constexpr int kDnWarps = 8;
-
 // One CTA: 16 output columns (rows of every chosen expert's W2), all tokens.
 // Runs of two K blocks go to the warps in turn, over all entries; a warp adds
 // weight * scales * product to its token columns, and the warps' sums are
@@ -209,8 +207,8 @@ constexpr int kDnWarps = 8;
 // The gate/up kernel has passed its own wait before this one can start, so all
 // but its output (h) is complete: the list and the routing weights are made
 // before the wait.
-template <bool GATHER>
-__global__ void __launch_bounds__(32 * kDnWarps, 3) experts_down_kernel(const ExpertsParams p) {
+template <bool GATHER, int kDnWarps>
+__global__ void __launch_bounds__(32 * kDnWarps, 24 / kDnWarps) experts_down_kernel(const ExpertsParams p) {
   __shared__ ExpertList L;
   __shared__ float rw[kMaxList][8];  // routing weight of (entry, column)
   __shared__ float sums[kDnWarps][16][GATHER ? 17 : 9];  // row, token
@@ -336,8 +334,13 @@ cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weig
   const cudaError_t e = launch_pdl(experts_gateup_kernel, dim3((unsigned)std::min<int64_t>(units, sms)), dim3(kGuThreads),
                                    0, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(d.T <= 8 ? experts_down_kernel<false> : experts_down_kernel<true>, dim3(d.H / 16), dim3(32 * kDnWarps), 0,
-                    s, p);
+  // an SM runs 24 warps of the down kernel: as one CTA where the output columns
+  // make at most two a SM (8 tokens, H = 1024, I = 512, 32 experts: 14 us a call
+  // against 20), else as three (one token, H = 7168: 68 us against 75)
+  const dim3 grid(d.H / 16);
+  if (d.H / 16 <= 2 * sms)
+    return launch_pdl(d.T <= 8 ? experts_down_kernel<false, 24> : experts_down_kernel<true, 24>, grid, dim3(768), 0, s, p);
+  return launch_pdl(d.T <= 8 ? experts_down_kernel<false, 8> : experts_down_kernel<true, 8>, grid, dim3(256), 0, s, p);
 }
 
 }  // namespace fp4moe
