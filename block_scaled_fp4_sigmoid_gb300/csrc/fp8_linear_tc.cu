@@ -22,8 +22,9 @@
 // tiles in turn, 256 weight rows wide where that fills whole rounds and 128
 // wide for the rest (a launch of its own that starts where the first one's
 // CTAs run out of tiles).  With fewer, a cluster of S CTAs shares a tile, each
-// with a run of its K blocks; the sums meet in distributed shared memory,
-// where each CTA adds a slice of the columns over the runs, in the order of K.
+// with a run of its K blocks; each sends the others their slices of the columns
+// through distributed shared memory and adds its own over the runs, in the order
+// of K.
 //
 // Warp roles: warp 0 TMA producer, warps 1 and 2 MMA issuers, warps 4-11 epilogue
 // (warp groups of their own, with the larger register share).  Every wait
@@ -53,25 +54,28 @@ struct TcPlan {
 constexpr int kTcCtas = 152;    // one CTA per SM
 
 struct TcParams {
-  CUtensorMap tmx, tmw;
+  CUtensorMap tmx, tmw;    // boxes of whole tiles
+  CUtensorMap tmx1, tmw1;  // the last token tile's and the last weight tile's: the rows that exist
   const float *xs, *ws;
   uint8_t* out;
   int64_t out_ld;
   int32_t* status;        // null: linear_status
   TcPlan plan;
   int T, N;
+  int xbytes, wbytes;     // of the last tiles' boxes
   int out_fp32, vec;      // vec: 16-byte stores are aligned
   int second;             // the second launch of a call: joins the first one's end, not its start
 };
 
-template <int BN>
+template <int BN, bool SPLIT>
 struct TcCfg {
   static constexpr int kEpiWarps = 8, kThreads = 128 + 32 * kEpiWarps;  // warp 3 idles
   static constexpr int kCols = BN / 2;  // columns of one epilogue warp
   static constexpr int kABytes = 128 * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = BN == 256 ? 4 : SPLIT ? 5 : 6;
   static constexpr int kBufs = 512 / BN;              // all of tensor memory
-  static constexpr int kStaging = kEpiWarps * 4096;   // 32 rows x 128 bytes per epilogue warp
+  // 32 rows x 128 bytes per epilogue warp; SPLIT: the other CTAs' sums of this one's slice, 7/8 of a tile at most
+  static constexpr int kStaging = SPLIT ? 128 * BN * 4 * 7 / 8 : kEpiWarps * 4096;
   static constexpr int kSmem = kStages * kStage + kStaging + 1024;
   // launched with 168 registers a thread (384 threads); 128 x 40 + 256 x 232 = 384 x 168
   static constexpr int kCtlRegs = 40, kEpiRegs = 232;
@@ -108,16 +112,13 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(s));
 }
 
-// 16 bytes at this CTA's shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr, int rank) {
-  float4 v;
+// 16 bytes to this CTA's shared-memory offset in CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, int rank, const uint32_t* v) {
   asm volatile(
-      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(addr), "r"(rank)
+      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "st.shared::cluster.v4.b32 [ra], {%2, %3, %4, %5};\n\t}" ::"r"(addr),
+      "r"(rank), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
       : "memory");
-  return v;
 }
 
 // A scale load that stays where it is written (volatile): moved down to its
@@ -185,9 +186,85 @@ __device__ __forceinline__ void store_rows(const TcParams& p, const uint8_t* stg
   }
 }
 
+// A cluster's join.  Of a tile's COLS columns of this thread's row (acc: pairs) a
+// slice falls to each of the S CTAs: a thread sends the others theirs, then sums
+// its own over the CTAs in the order of K.  `at`: vector 0 of this thread in
+// the region for the others' sums, where CTA s of the others has the s-th part.
+// Sent, not fetched: with the loads of a slice from every CTA the join took 4.5
+// us, with stores 2.2 (128 x 7168 x 7168, two CTAs a tile: 17.5 -> 16.1 us; 333 x 7168 x
+// 2000, four: 15.7 -> 13.1).
+template <int COLS, int S>
+__device__ __forceinline__ void join_slices(const TcParams& p, const uint64_t* acc, uint32_t at, int rank, int row,
+                                            int col) {
+  constexpr int kVecs = COLS / 4 / S;  // of 4 columns
+  uint32_t own[kVecs][4];
+#pragma unroll
+  for (int r = 0; r < S; ++r)
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      uint32_t w[4];
+      unpack2(acc[2 * (kVecs * r + i)], w[0], w[1]);
+      unpack2(acc[2 * (kVecs * r + i) + 1], w[2], w[3]);
+      if (r == rank) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) own[i][j] = w[j];
+      } else if (row < p.T) {
+        st_cluster(at + 4096u * (kVecs * (rank - (rank > r)) + i), r, w);
+      }
+    }
+  __syncwarp();
+  cluster_arrive_wait();
+  if (row >= p.T) return;
+  col += 4 * kVecs * rank;
+  const int esz = p.out_fp32 ? 4 : 2;
+  uint8_t* dst = p.out + ((int64_t)row * p.out_ld + col) * esz;
+#pragma unroll
+  for (int i = 0; i < kVecs; i += 2) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll
+    for (int r = 0; r < S; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[4];
+        if (r == rank) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = own[i + h][j];
+        } else {
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at + 4096u * (kVecs * (r - (r > rank)) + i + h))
+                       : "memory");
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * h + j] += __uint_as_float(w[j]);
+      }
+    const int n = min(8, p.N - col - 4 * i);
+    if (p.vec && n == 8) {
+      if (p.out_fp32) {
+        reinterpret_cast<float4*>(dst)[i] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(dst)[i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4*>(dst + 8 * i) =
+            make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) {
+          if (p.out_fp32)
+            reinterpret_cast<float*>(dst)[4 * i + j] = v[j];
+          else
+            reinterpret_cast<uint16_t*>(dst)[4 * i + j] = f32_to_bf16_rn(v[j]);
+        }
+    }
+  }
+}
+
 template <int BN, bool SPLIT>
-__global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const __grid_constant__ TcParams p) {
-  using C = TcCfg<BN>;
+__global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kernel(const __grid_constant__ TcParams p) {
+  using C = TcCfg<BN, SPLIT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
   __shared__ __align__(8) uint64_t bar_tfull[C::kBufs], bar_tempty[C::kBufs], bar_done;
@@ -222,6 +299,8 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&p.tmx);
     prefetch_tmap(&p.tmw);
+    prefetch_tmap(&p.tmx1);
+    prefetch_tmap(&p.tmw1);
   }
   // The second launch of a call begins once every CTA of the first has passed
   // its own wait, so its inputs are complete; it waits for the first at its end,
@@ -233,6 +312,7 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
+  if constexpr (SPLIT) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int* abort_v = &abort_flag;
@@ -255,17 +335,24 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
       for (int tile = first; ok && tile < tiles; tile += step) {
         int mt, nt;
         tile_at(tile, p.plan.mtiles, p.plan.ntiles, mt, nt);
+        // Boxes end with the rows that exist.  What shared memory holds past them goes
+        // through the MMAs into rows and columns that are not stored.  (Boxes of whole
+        // tiles, zeros filled in past the end, arrive at half the rate: 16 x 7168 x
+        // 18432 took 33 us, now 24.)
+        const bool x1 = mt + 1 == p.plan.mtiles, w1 = nt + 1 == p.plan.ntiles;
+        const CUtensorMap *tmx = x1 ? &p.tmx1 : &p.tmx, *tmw = w1 ? &p.tmw1 : &p.tmw;
+        const uint32_t bytes = (x1 ? p.xbytes : C::kABytes) + (w1 ? p.wbytes : C::kBBytes);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_abortable(smem_u32(&bar_empty[stage]), phase ^ 1u, kWaitLimitNs, abort_v)) {
             ok = false;
             break;
           }
           const uint32_t fb = smem_u32(&bar_full[stage]), base = sbase + stage * C::kStage;
-          mbar_arrive_expect_tx(fb, C::kStage);
+          mbar_arrive_expect_tx(fb, bytes);
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-          tma_load_2d(base, &p.tmx, fb, kb * 128, mt * 128);
-          tma_load_2d(base + C::kABytes, &p.tmw, fb, kb * 128, nt * BN);
+          tma_load_2d(base, tmx, fb, kb * 128, mt * 128);
+          tma_load_2d(base + C::kABytes, tmw, fb, kb * 128, nt * BN);
           if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
       }
@@ -298,7 +385,7 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
           tc_mma_f8_elect(tmem + buf * BN, a0 + so + 2 * j, b0 + so + 2 * j, idesc_f8(BN), j ? 1u : 0u);
         tc_commit_elect(smem_u32(&bar_empty[stage]));
         tc_commit_elect(smem_u32(&bar_tfull[buf]));
-        stage += 2;  // stages and buffers are even in number
+        stage += 2;
         if (stage >= C::kStages) { stage -= C::kStages; phase ^= 1u; }
         buf += 2;
         if (buf >= C::kBufs) { buf -= C::kBufs; bphase ^= 1u; }
@@ -400,70 +487,25 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
     if (!ok && lane == 0) timed_out();
     __syncwarp();
     if constexpr (SPLIT) {
-      // the pipeline's stages have been read: they take the CTA's sums,
-      // vector i (4 columns) of epilogue thread et at 16 (256 i + et)
-      const uint32_t mine = sbase + 16u * (threadIdx.x - 128);
-#pragma unroll
-      for (int i = 0; i < C::kCols / 4; ++i) {
-        uint32_t w[4];
-        unpack2(acc[2 * i], w[0], w[1]);
-        unpack2(acc[2 * i + 1], w[2], w[3]);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + 4096u * i), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3])
-                     : "memory");
-      }
+      cluster_wait();  // every CTA of the cluster has begun
+      const int row = t0 + lane;
+      const uint32_t at = sbase + C::kStages * C::kStage + 16u * (threadIdx.x - 128);
+      if (S == 2) join_slices<C::kCols, 2>(p, acc, at, rank, row, n0);
+      if (S == 4) join_slices<C::kCols, 4>(p, acc, at, rank, row, n0);
+      if (S == 8) join_slices<C::kCols, 8>(p, acc, at, rank, row, n0);
     }
   }
   if constexpr (SPLIT) {
-    __syncwarp();
-    cluster_arrive_wait();  // every CTA's sums are in its shared memory
-    if (warp >= 4 && !*abort_v) {
-      const int q = warp & 3, c0 = ((warp - 4) >> 2) * C::kCols, vs = C::kCols / 4 / S;  // vectors of this CTA's slice
-      const uint32_t at = sbase + 16u * (threadIdx.x - 128);
-      int mt, nt;
-      tile_at(first, p.plan.mtiles, p.plan.ntiles, mt, nt);
-      const int row = mt * 128 + 32 * q + lane, col = nt * BN + c0 + 4 * vs * rank;
-      const int esz = p.out_fp32 ? 4 : 2;
-      uint8_t* dst = p.out + ((int64_t)row * p.out_ld + col) * esz;
-      for (int i = 0; i < vs; i += 2) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        for (int r = 0; r < S; ++r) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 w = ld_cluster(at + 4096u * (vs * rank + i + j), r);
-            v[4 * j] += w.x, v[4 * j + 1] += w.y, v[4 * j + 2] += w.z, v[4 * j + 3] += w.w;
-          }
-        }
-        const int n = row < p.T ? min(8, p.N - col - 4 * i) : 0;
-        if (p.vec && n == 8) {
-          if (p.out_fp32) {
-            reinterpret_cast<float4*>(dst)[i] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(dst)[i + 1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            *reinterpret_cast<uint4*>(dst + 8 * i) =
-                make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n) {
-              if (p.out_fp32)
-                reinterpret_cast<float*>(dst)[4 * i + j] = v[j];
-              else
-                reinterpret_cast<uint16_t*>(dst)[4 * i + j] = f32_to_bf16_rn(v[j]);
-            }
-        }
-      }
+    if (warp < 4) {
+      __syncwarp();
+      cluster_wait();
+      cluster_arrive_wait();
     }
-    __syncwarp();
   }
 
+  // (SPLIT: the cluster's barrier, after every CTA's last fetch from tensor memory and last store to another)
   tc_fence_before();
-  // (SPLIT: no CTA leaves while another reads its shared memory)
-  if constexpr (SPLIT) cluster_arrive_wait();
-  else __syncthreads();
+  if constexpr (!SPLIT) __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -473,26 +515,29 @@ __global__ void __launch_bounds__(TcCfg<BN>::kThreads, 1) linear_tc_kernel(const
 
 template <int BN, bool SPLIT>
 cudaError_t launch_tc(const LinearFp8Args& a, int split, bool second, cudaStream_t s) {
-  using C = TcCfg<BN>;
+  using C = TcCfg<BN, SPLIT>;
   auto k = linear_tc_kernel<BN, SPLIT>;
   TcParams p;
   memset(&p, 0, sizeof(p));
-  {
-    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.T}, strides[1] = {(uint64_t)a.K};
-    const uint32_t box[2] = {128, 128};
-    if (!encode_tmap_u8(&p.tmx, a.xq, 2, dims, strides, box, true)) return cudaErrorInvalidValue;
-  }
-  {
-    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.N}, strides[1] = {(uint64_t)a.K};
-    const uint32_t box[2] = {128, (uint32_t)BN};
-    if (!encode_tmap_u8(&p.tmw, a.w, 2, dims, strides, box, true)) return cudaErrorInvalidValue;
-  }
+  p.plan = {split, blocks128(a.K), (a.T + 127) / 128, (a.N + BN - 1) / BN};
+  const uint32_t xrows = (uint32_t)(a.T - 128 * (p.plan.mtiles - 1)), wrows = (uint32_t)(a.N - BN * (p.plan.ntiles - 1));
+  p.xbytes = (int)(128 * xrows);
+  p.wbytes = (int)(128 * wrows);
+  auto map = [&](CUtensorMap* m, const uint8_t* base, int rows, uint32_t box_rows) {
+    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)rows}, strides[1] = {(uint64_t)a.K};
+    const uint32_t box[2] = {128, box_rows};
+    return encode_tmap_u8(m, base, 2, dims, strides, box, true);
+  };
+  if (!map(&p.tmx1, a.xq, a.T, xrows) || !map(&p.tmw1, a.w, a.N, wrows)) return cudaErrorInvalidValue;
+  p.tmx = p.tmx1;
+  p.tmw = p.tmw1;
+  if (p.plan.mtiles > 1 && xrows != 128 && !map(&p.tmx, a.xq, a.T, 128)) return cudaErrorInvalidValue;
+  if (p.plan.ntiles > 1 && wrows != BN && !map(&p.tmw, a.w, a.N, BN)) return cudaErrorInvalidValue;
   p.xs = a.xs;
   p.ws = a.ws;
   p.out = static_cast<uint8_t*>(a.out);
   p.out_ld = a.out_ld;
   p.status = static_cast<int32_t*>(a.scratch);
-  p.plan = {split, blocks128(a.K), (a.T + 127) / 128, (a.N + BN - 1) / BN};
   p.T = a.T;
   p.N = a.N;
   p.out_fp32 = a.out_fp32 ? 1 : 0;
@@ -518,22 +563,23 @@ cudaError_t launch_tc(const LinearFp8Args& a, int split, bool second, cudaStream
 // How a call is run: columns [0, wide) in tiles of 256, the rest in tiles of
 // 128; split > 1: all of it in tiles of 128 shared by `split` CTAs.  Chosen by
 // the time per K block of a tile (measured: 0.43 us 256 wide, 0.29 us 128
-// wide; joining a split tile 3.5 us) and the rounds that the tiles make on 152
-// SMs.  A split tile's CTAs are a cluster, and no more clusters are taken than
-// run at the same time (measured: 15 of 8, 36 and more of 4, 76 of 2; a second
-// round doubles the time, 128 x 4096 x 1920 9.1 us, x 2048 15.9).
+// wide; joining a split tile 1.5 us for few tokens, 2.9 for 128) and the rounds
+// that the tiles make on 152 SMs.  A split tile's CTAs are a cluster, and no more
+// clusters are taken than run at the same time (measured: 15 of 8, 36 and more
+// of 4, 76 of 2; with more, a second round doubles the time).
 struct TcChoice {
   int wide, split;
   int64_t cost;  // in 10 ns, without the launch
 };
 TcChoice choose(int T, int K, int N) {
-  constexpr int64_t kT256 = 43, kT128 = 29, kJoin = 350;  // 10 ns
+  constexpr int64_t kT256 = 43, kT128 = 29;  // 10 ns
+  const int64_t join = 130 + std::min(T, 128) * 5 / 4;
   const int64_t nb = blocks128(K), mt = (T + 127) / 128, sms = kTcCtas;
   const int64_t n128 = (N + 127) / 128;
   TcChoice best{0, 1, 0};
   int64_t cost = (mt * n128 + sms - 1) / sms * nb * kT128;
   for (int split = 2; split <= 8; split *= 2) {
-    const int64_t c = (nb + split - 1) / split * kT128 + kJoin;
+    const int64_t c = (nb + split - 1) / split * kT128 + join;
     if (mt * n128 <= (split == 2 ? 75 : split == 4 ? 36 : 14) && nb >= 2 * split && c < cost) cost = c, best = {0, split, 0};
   }
   const int64_t all = (N + 255) / 256;
