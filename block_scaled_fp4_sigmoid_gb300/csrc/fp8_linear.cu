@@ -103,31 +103,32 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
 
 size_t linear_fp8_workspace(int, int, int) { return 256; }
 
-// Up to 16 tokens are streamed (measured at 7168 x 7168: 16 tokens 13 us against
-// 20 us of the tensor-core kernel; 32 tokens 37 us against 16 us).  From 17 to
-// 128 the weights would be streamed once for every 16 tokens, which small
-// products still do sooner than the tensor-core kernel starts and joins its
-// parts (64 x 2048 x 512: 2.8 us against 7.4, 32 x 7168 x 576 5.1 against 8.8; but
-// 32 x 7168 x 2112 12.4 against 9.9): the smaller of two estimates, both fitted to
-// such measurements, decides.
-//
+// Weights streamed into mma.sync or through shared memory into the tensor cores: the
+// former starts 1 to 2 us sooner, the latter has no rounds of CTAs each with
+// a latency of its own, and reads the weights once where the former reads them for
+// every 16 tokens.  Up to 128 tokens the smaller of two estimates decides, both
+// fitted to measurements (stream, tensor cores): 8 x 7168 x 36864 44.0, 44.5 us;
+// 8 x 1024 x 131072 36.7, 26.8; 16 x 7168 x 36864 74.7, 44.8; 16 x 7168 x 2112 6.8,
+// 7.9; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  In 10 ns:
+static int64_t stream_cost(const LinearFp8Args& a) {
+  const int64_t sms = 152, nb = blocks128(a.K), ctas = (a.N + 15) / 16 * (a.T > 8 ? (a.T + 15) / 16 : 1);
+  const int64_t rounds = (ctas + 3 * sms - 1) / (3 * sms);  // of three CTAs an SM
+  if (a.T > 8) return ctas <= sms ? 160 + nb * 7 : rounds * (150 + nb * 19);
+  return std::max(ctas <= 2 * sms ? 150 + nb * 5 : (ctas <= 4 * sms ? 1 : rounds) * (140 + nb * 8), (int64_t)a.K * a.N / 60000);  // (6 TB/s)
+}
+
 // The more CTAs share an SM, the fewer registers and so the fewer loads in
-// flight a warp.  With more row tiles than that, two blocks a run and three CTAs
+// flight a warp.  With row tiles for all of them, two blocks a run and three CTAs
 // an SM stream best, unless the last round of CTAs would be much emptier than
 // with one block and four CTAs (7168 x 7168, 448 tiles, 8 tokens: 11.0 us against
 // 11.9; 7168 x 36864, 2304 tiles: 49.6 against 43.9).  Where the tiles hardly
 // cover the SMs, four blocks a run (7168 x 2112, 132 tiles: 4.4 us against 5.2;
 // 16 tokens 6.9 against 10.1).
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
-  const int64_t rows = (a.N + 15) / 16, sms = 152, nb = blocks128(a.K);
+  const int64_t rows = (a.N + 15) / 16, sms = 152;
   const int64_t chunks = a.T > 8 ? (a.T + 15) / 16 : 1, ctas = rows * chunks;
-  if (a.T > 16) {
-    // in 10 ns; the launches differ by about 1 us
-    const int64_t stream = ctas <= sms ? nb * 52 / 10
-                                       : std::max((ctas + 3 * sms - 1) / (3 * sms) * nb * 35 / 2,
-                                                  chunks * a.N * (int64_t)a.K / 40000);  // (weights at 4 TB/s)
-    if (a.T > 128 || stream > linear_fp8_tc_cost(a.T, a.K, a.N) + 100) return launch_linear_fp8_tc(a, s);
-  }
+  if (a.T > 128 || stream_cost(a) > std::max(linear_fp8_tc_cost(a.T, a.K, a.N), (int64_t)a.K * a.N / 56000) + 250)
+    return launch_linear_fp8_tc(a, s);
   const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
                        a.out_fp32 ? 1 : 0};
   const dim3 grid((unsigned)rows, (unsigned)chunks), block(32 * kStreamWarps);
