@@ -127,8 +127,9 @@ static int64_t stream_cost(const LinearFp8Args& a) {
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
   const int64_t rows = (a.N + 15) / 16, sms = 152;
   const int64_t chunks = a.T > 8 ? (a.T + 15) / 16 : 1, ctas = rows * chunks;
-  if (a.T > 128 || stream_cost(a) > std::max(linear_fp8_tc_cost(a.T, a.K, a.N), (int64_t)a.K * a.N / 56000) + 250)
-    return launch_linear_fp8_tc(a, s);
+  if (a.T > 128) return launch_linear_fp8_tc(a, s);
+  const int64_t stream = stream_cost(a) - 250;  // (what the tensor cores start later)
+  if (stream > (int64_t)a.K * a.N / 56000 && stream > linear_fp8_tc_cost(a.T, a.K, a.N)) return launch_linear_fp8_tc(a, s);
   const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
                        a.out_fp32 ? 1 : 0};
   const dim3 grid((unsigned)rows, (unsigned)chunks), block(32 * kStreamWarps);

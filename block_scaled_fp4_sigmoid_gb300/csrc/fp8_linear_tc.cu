@@ -582,6 +582,8 @@ TcChoice choose(int T, int K, int N) {
     const int64_t c = (nb + split - 1) / split * kT128 + join;
     if (mt * n128 <= (split == 2 ? 75 : split == 4 ? 36 : 14) && nb >= 2 * split && c < cost) cost = c, best = {0, split, 0};
   }
+  best.cost = cost;
+  if (mt * n128 <= sms) return best;  // one round of 128: wider tiles take longer
   const int64_t all = (N + 255) / 256;
   for (int64_t w = all; w > 0 && (all - w) * mt <= 2 * sms; --w) {  // w tiles of 256, the rest (two rounds at most) of 128
     const int64_t rest = std::max<int64_t>(0, n128 - 2 * w) * mt, t = w * mt, full = t / sms, late = t % sms;
