@@ -139,50 +139,90 @@ __device__ __forceinline__ void tile_at(int tile, int mtiles, int ntiles, int& m
   mt = g * kGroupM + in - nt * gm;
 }
 
-// One warp's 32 staged rows (128 bytes each, 16-byte pieces xor-swizzled by the
-// row) to columns [col, col + cols) of rows row.. of out, where these are inside
-// it: whole aligned 16-byte vectors, eight lanes a row, and element by element
-// what sticks out of them at either end (a row of an odd width starts anywhere;
-// with elements alone 3228 x 2304 x 10881 took 147 us).
-__device__ __forceinline__ void store_rows(const TcParams& p, const uint8_t* stg, int lane, int row, int col, int cols) {
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_one(const TcParams& p, uint8_t* d, uint32_t v) {
+  if (p.out_fp32)
+    *reinterpret_cast<uint32_t*>(d) = v;
+  else
+    *reinterpret_cast<uint16_t*>(d) = (uint16_t)v;
+}
+
+// The 16 bytes of (lo, hi) from byte `at`, an even number below 16.
+__device__ __forceinline__ uint4 bytes_from(const uint4& lo, const uint4& hi, int at) {
+  uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+  if (at & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = hi.w;
+  if (at & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+  const uint32_t sh = (at & 2) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                    __funnelshift_r(w[3], w[4], sh));
+}
+
+// One warp's 32 staged rows (at shared-memory address stg, 128 bytes each, 16-byte
+// pieces xor-swizzled by the row) to columns [col, col + cols) of rows row.. of
+// out, where these are inside it.  Eight lanes a row, whole aligned 16-byte
+// vectors; a row of an odd width starts anywhere, so its vectors are put together
+// from two pieces, and what sticks out of them at either end goes element by
+// element (eight of bf16 in 128 bytes: one a lane).  Loads of several rows
+// before their stores: one row at a time waits for shared memory each time.
+__device__ __forceinline__ void store_rows(const TcParams& p, uint32_t stg, int lane, int row, int col, int cols) {
   const int esz = p.out_fp32 ? 4 : 2, nbytes = min(cols, p.N - col) * esz, nrow = min(32, p.T - row);
   if (nbytes <= 0) return;
   uint8_t* dst = p.out + ((int64_t)row * p.out_ld + col) * esz;
   const int64_t ld = p.out_ld * esz;
-  if (p.vec && nbytes == 128) {
-    uint8_t* d = dst + (lane >> 3) * ld + 16 * (lane & 7);
+  const int l = lane & 7, r0 = lane >> 3;
+  if (p.vec && nbytes % 16 == 0) {
+    uint8_t* d = dst + r0 * ld + 16 * l;
+    uint4 w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = (lane >> 3) + 4 * i;
-      const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-      if (r < nrow) *reinterpret_cast<uint4*>(d + 4 * i * ld) = w;
-    }
+    for (int i = 0; i < 8; ++i) w[i] = lds128(stg + (r0 + 4 * i) * 128 + ((l ^ ((r0 + 4 * i) & 7)) << 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + 4 * i < nrow && 16 * l < nbytes) *reinterpret_cast<uint4*>(d + 4 * i * ld) = w[i];
     return;
   }
-  auto at = [&](int r, int byte) { return stg + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15); };
-#pragma unroll 1
-  for (int r = lane >> 3; r < nrow; r += 4) {
-    uint8_t* d = dst + r * ld;
-    const int l = lane & 7, off = (int)(reinterpret_cast<uintptr_t>(d) & 15u);  // of the row in its first vector
-    const int head = off ? min(16 - off, nbytes) : 0, tail = max(head, ((off + nbytes) & ~15) - off);
-    const int byte = head + 16 * l;  // where this lane's vector starts
-    if (byte < tail) {
-      uint32_t w[5];  // the five words that hold it
+  // Of a row that starts off bytes into a vector, the window's first n16 bytes are
+  // n16 / 16 - 1 whole vectors, and of the elements of its first and last piece
+  // those outside them: 16 bytes together.
+  const int n16 = nbytes & ~15, rest = n16 + l * esz;
+  uint8_t* d = dst + r0 * ld;
+  const uint32_t row_at = stg + r0 * 128;
+  constexpr int kRows = 4;  // a lane's rows at a time
 #pragma unroll
-      for (int k = 0; k < 5; ++k)
-        w[k] = k < 4 || (byte & 2) ? *reinterpret_cast<const uint32_t*>(at(r, (byte & ~3) + 4 * k)) : 0u;
-      const uint32_t sh = (byte & 2) * 8;
-      *reinterpret_cast<uint4*>(d + byte) = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                                                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+  for (int h = 0; h < 8; h += kRows) {
+    uint4 lo[kRows], hi[kRows];
+    uint32_t e[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const uint32_t at = row_at + 512 * (h + i), x = (r0 + 4 * i) & 7;  // (its swizzle)
+      const int off = (int)(reinterpret_cast<uintptr_t>(d + 4 * i * ld) & 15u), eb = l * esz;
+      lo[i] = lds128(at + ((l ^ x) << 4));
+      hi[i] = lds128(at + (((l + 1) & 7) ^ x) * 16);
+      const int piece = eb < 16 - off ? 0 : (n16 >> 4) - 1;
+      e[i] = lds32(at + (((piece & 7) ^ x) << 4) + (eb & 12)) >> ((eb & 2) * 8);
     }
-    auto one = [&](int byte) {
-      if (p.out_fp32)
-        *reinterpret_cast<uint32_t*>(d + byte) = *reinterpret_cast<const uint32_t*>(at(r, byte));
-      else
-        *reinterpret_cast<uint16_t*>(d + byte) = *reinterpret_cast<const uint16_t*>(at(r, byte));
-    };
-    if (l * esz < head) one(l * esz);
-    if (tail + l * esz < nbytes) one(tail + l * esz);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = r0 + 4 * (h + i), eb = l * esz;
+      const int off = (int)(reinterpret_cast<uintptr_t>(d) & 15u), head = (16 - off) & 15;
+      if (r < nrow) {
+        if (16 * l < n16 - (off ? 16 : 0)) *reinterpret_cast<uint4*>(d + head + 16 * l) = bytes_from(lo[i], hi[i], head);
+        if (off && eb < 16 && n16) store_one(p, d + (eb < head ? eb : n16 - 16 + eb), e[i]);
+        if (rest < nbytes)
+          store_one(p, d + rest,
+                    lds32(row_at + 512 * (h + i) + (((rest >> 4) ^ r) & 7) * 16 + (rest & 12)) >> ((rest & 2) * 8));
+      }
+      d += 4 * ld;
+    }
   }
 }
 
@@ -194,8 +234,8 @@ __device__ __forceinline__ void store_rows(const TcParams& p, const uint8_t* stg
 // us, with stores 2.2 (128 x 7168 x 7168, two CTAs a tile: 17.5 -> 16.1 us; 333 x 7168 x
 // 2000, four: 15.7 -> 13.1).
 template <int COLS, int S>
-__device__ __forceinline__ void join_slices(const TcParams& p, const uint64_t* acc, uint32_t at, int rank, int row,
-                                            int col) {
+__device__ __forceinline__ void join_slices(const TcParams& p, const uint64_t* acc, uint32_t at, uint8_t* stg, int rank,
+                                            int lane, int row, int col) {
   constexpr int kVecs = COLS / 4 / S;  // of 4 columns
   uint32_t own[kVecs][4];
 #pragma unroll
@@ -208,58 +248,45 @@ __device__ __forceinline__ void join_slices(const TcParams& p, const uint64_t* a
       if (r == rank) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) own[i][j] = w[j];
-      } else if (row < p.T) {
+      } else if (row + lane < p.T) {
         st_cluster(at + 4096u * (kVecs * (rank - (rank > r)) + i), r, w);
       }
     }
   __syncwarp();
   cluster_arrive_wait();
-  if (row >= p.T) return;
-  col += 4 * kVecs * rank;
-  const int esz = p.out_fp32 ? 4 : 2;
-  uint8_t* dst = p.out + ((int64_t)row * p.out_ld + col) * esz;
+  float v[4 * kVecs];
 #pragma unroll
-  for (int i = 0; i < kVecs; i += 2) {
-    float v[8];
+  for (int j = 0; j < 4 * kVecs; ++j) v[j] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  for (int r = 0; r < S; ++r)
 #pragma unroll
-    for (int r = 0; r < S; ++r)
+    for (int i = 0; i < kVecs; ++i) {
+      uint32_t w[4];
+      if (r == rank) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[4];
-        if (r == rank) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = own[i + h][j];
-        } else {
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(at + 4096u * (kVecs * (r - (r > rank)) + i + h))
-                       : "memory");
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * h + j] += __uint_as_float(w[j]);
-      }
-    const int n = min(8, p.N - col - 4 * i);
-    if (p.vec && n == 8) {
-      if (p.out_fp32) {
-        reinterpret_cast<float4*>(dst)[i] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(dst)[i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+        for (int j = 0; j < 4; ++j) w[j] = own[i][j];
       } else {
-        *reinterpret_cast<uint4*>(dst + 8 * i) =
-            make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at + 4096u * (kVecs * (r - (r > rank)) + i))
+                     : "memory");
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) {
-          if (p.out_fp32)
-            reinterpret_cast<float*>(dst)[4 * i + j] = v[j];
-          else
-            reinterpret_cast<uint16_t*>(dst)[4 * i + j] = f32_to_bf16_rn(v[j]);
-        }
+      for (int j = 0; j < 4; ++j) v[4 * i + j] += __uint_as_float(w[j]);
     }
+  // 4 kVecs columns of 32 rows, through shared memory
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    if (p.out_fp32)
+      *reinterpret_cast<float4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    else if (i % 2 == 0)
+      *reinterpret_cast<uint4*>(stg + lane * 128 + (((i / 2) ^ (lane & 7)) << 4)) =
+          make_uint4(bf16x2_rn(v[4 * i], v[4 * i + 1]), bf16x2_rn(v[4 * i + 2], v[4 * i + 3]),
+                     bf16x2_rn(v[4 * i + 4], v[4 * i + 5]), bf16x2_rn(v[4 * i + 6], v[4 * i + 7]));
   }
+  __syncwarp();
+  store_rows(p, smem_u32(stg), lane, row, col + 4 * kVecs * rank, 4 * kVecs);
 }
 
 template <int BN, bool SPLIT>
@@ -480,7 +507,7 @@ __global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kerne
           *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
-        store_rows(p, stg, lane, st0, nc, per);
+        store_rows(p, smem_u32(stg), lane, st0, nc, per);
         __syncwarp();
       }
     }
@@ -488,11 +515,11 @@ __global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kerne
     __syncwarp();
     if constexpr (SPLIT) {
       cluster_wait();  // every CTA of the cluster has begun
-      const int row = t0 + lane;
       const uint32_t at = sbase + C::kStages * C::kStage + 16u * (threadIdx.x - 128);
-      if (S == 2) join_slices<C::kCols, 2>(p, acc, at, rank, row, n0);
-      if (S == 4) join_slices<C::kCols, 4>(p, acc, at, rank, row, n0);
-      if (S == 8) join_slices<C::kCols, 8>(p, acc, at, rank, row, n0);
+      stg = smem_raw + (sbase - smem_u32(smem_raw)) + (warp - 4) * 4096;  // the pipeline's stages have been read
+      if (S == 2) join_slices<C::kCols, 2>(p, acc, at, stg, rank, lane, t0, n0);
+      if (S == 4) join_slices<C::kCols, 4>(p, acc, at, stg, rank, lane, t0, n0);
+      if (S == 8) join_slices<C::kCols, 8>(p, acc, at, stg, rank, lane, t0, n0);
     }
   }
   if constexpr (SPLIT) {

@@ -220,6 +220,24 @@ def test_linear_into_aligned_columns_of_a_wider_output(ops, T, K, N, fp32):
     assert bool((wide == 7.0).all())
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("at", [0, 1, 6])
+@pytest.mark.parametrize("T,K,N", [(40, 14336, 291), (130, 2048, 811), (257, 4096, 1501), (200, 4096, 4099), (163, 576, 2925),
+                                   (9, 1024, 8191), (600, 512, 5001), (70, 2048, 1029)])
+def test_linear_rows_that_start_anywhere(ops, T, K, N, at, fp32):
+    """Odd widths, first columns off 16 bytes, few rows in the last tile: tiles of one CTA and of
+    clusters of two, four and eight, against 64 bits; nothing else is written."""
+    import torch
+    xq, xs, wq, ws = linear_inputs(T, K, N, T + N)
+    y, S = B.linear(xq, xs, wq, ws)
+    wide = torch.full((T + 2, N + at + 5), 7.0, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+    ops.linear_fp8_block(*[dev(v) for v in (xq, xs, wq, ws)], out=wide[1:T + 1, at:at + N])
+    bad = np.abs(f64(wide[1:T + 1, at:at + N]) - y) > (U_F32 if fp32 else U_BF16) * np.abs(y) + B.ACC * S
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4])
+    wide[1:T + 1, at:at + N] = 7.0
+    assert bool((wide == 7.0).all())
+
+
 @pytest.mark.parametrize("T,K,N", [(2, 256, 40), (40, 384, 300), (260, 512, 300)])
 def test_linear_nan_stays_in_its_row_and_column(ops, T, K, N):
     xq, xs, wq, ws = linear_inputs(T, K, N, 6)
