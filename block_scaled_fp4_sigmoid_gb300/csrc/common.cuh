@@ -270,8 +270,6 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -395,13 +393,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n) {
 }
 
 // Instruction descriptor of a dense E4M3 MMA: fp32 D, E4M3 A and B (format
-// code 0), both K-major, M = m (256: a CTA pair), N = n.
-__host__ __device__ constexpr uint32_t idesc_f8(uint32_t n, uint32_t m = 128) {
+// code 0), both K-major, M = 128, N = n.
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t n) {
   return 1u << 4              // D format: fp32
          | 0u << 7            // A format: E4M3
          | 0u << 10           // B format: E4M3
          | (n >> 3) << 17     // N / 8
-         | (m >> 4) << 24;    // M / 16
+         | (128u >> 4) << 24; // M / 16
 }
 
 // ---------------------------------------------------------------- FP4 / FP8 encoders

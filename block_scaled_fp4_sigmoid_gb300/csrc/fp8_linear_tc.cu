@@ -112,6 +112,10 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(s));
 }
 
+// The two halves of cluster_arrive_wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // 16 bytes to this CTA's shared-memory offset in CTA `rank` of the cluster.
 __device__ __forceinline__ void st_cluster(uint32_t addr, int rank, const uint32_t* v) {
   asm volatile(
