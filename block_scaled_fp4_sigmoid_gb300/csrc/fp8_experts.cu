@@ -28,6 +28,7 @@ struct ExpertsParams {
   float* hs;     // [entry * 8 + column, I / 128]
   uint16_t* out;
   int T, H, I, E, k, shared;
+  int split;  // CTAs that share a gate/up unit
 };
 
 struct ExpertList {
@@ -91,12 +92,28 @@ __device__ __forceinline__ void list_experts(const ExpertsParams& p, ExpertList&
 
 constexpr int kGuThreads = 512;
 
+// The two halves of cluster_arrive_wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A word to this CTA's shared-memory offset in CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\tst.shared::cluster.f32 [ra], %2;\n\t}" ::"r"(addr),
+      "r"(rank), "f"(v)
+      : "memory");
+}
+
 // One unit: 128 gate and 128 up rows (one scale block of h) of one entry.
 // Warp = 16 gate rows and the 16 up rows of the same h values, over every
 // second K block, straight from global memory into mma.sync operands: 8 loads
 // of 16 bytes in flight a lane.  HBM bound: 8 tokens over 384 experts (1.75
 // GB) in 262 us, 6.7 TB/s.
+//
+// SPLIT: a unit is shared by a cluster, each CTA with every split-th pair of K
+// blocks; CTA 0 gets the others' sums in its shared memory and finishes.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const ExpertsParams p) {
+  extern __shared__ __align__(16) float others[];  // SPLIT: [split - 1][8 warps][8][32]
   __shared__ ExpertList L;
   __shared__ float part[8][8][32];
   __shared__ float amax[8][8];
@@ -106,8 +123,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const Exp
   list_experts(p, L);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rg = warp & 7, kh = warp >> 3;
+  const int S = SPLIT ? p.split : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
   const int hb = p.H / kBlk, ib = p.I / kBlk, units = L.n * ib;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+  if constexpr (SPLIT) cluster_arrive();
+  for (int unit = (int)blockIdx.x / S; unit < units; unit += (int)gridDim.x / S) {
     const int u = unit / ib, b = unit - u * ib, e = L.e[u];
     const bool sh = e == p.E;
     const uint8_t* w = sh ? p.sh13 : p.w13 + (int64_t)e * 2 * p.I * p.H;
@@ -122,7 +141,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const Exp
 #pragma unroll
     for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
 #pragma unroll 1
-    for (int kb = kh; kb < hb; kb += 2) {
+    for (int kb = 2 * rank + kh; kb < hb; kb += 2 * S) {
       uint4 wv[2][4], x[2];
       const int64_t k0 = kb * kBlk + 16 * t;
 #pragma unroll
@@ -153,10 +172,36 @@ __global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const Exp
         for (int j = 0; j < 4; ++j) part[rg][m * 4 + j][lane] = acc[m][j];
     }
     __syncthreads();
+    if constexpr (SPLIT) {
+      if (!kh) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[m][j] += part[rg][m * 4 + j][lane];
+      }
+      cluster_wait();  // every CTA has begun, and CTA 0 has read the unit before
+      if (!kh && rank > 0) {
+        const uint32_t at = smem_u32(others + (((rank - 1) * 8 + rg) * 8) * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st_cluster(at + 128u * i, 0, acc[i >> 2][i & 3]);
+      }
+      __syncwarp();
+      cluster_arrive_wait();
+      if (!kh && rank == 0) {
+        for (int r = 0; r < S - 1; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += others[((r * 8 + rg) * 8 + i) * 32 + lane];
+      }
+      __syncwarp();
+      cluster_arrive();
+      if (rank > 0) continue;
+    }
     float h[4];
     if (!kh) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = swiglu(acc[0][j] + part[rg][j][lane], acc[1][j] + part[rg][4 + j][lane]);
+      for (int j = 0; j < 4; ++j)
+        h[j] = SPLIT ? swiglu(acc[0][j], acc[1][j])
+                     : swiglu(acc[0][j] + part[rg][j][lane], acc[1][j] + part[rg][4 + j][lane]);
       // columns 2t (j = 0, 2) and 2t + 1: largest |h| over the warp's 16 rows
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -189,6 +234,24 @@ __global__ void __launch_bounds__(kGuThreads, 1) experts_gateup_kernel(const Exp
             *reinterpret_cast<const uint4*>(&codes[col][c]);
     }
   }
+  if constexpr (SPLIT) cluster_wait();
+}
+
+// How many clusters of `split` CTAs run at the same time.
+int64_t clusters_of(int split) { return split == 1 ? 152 : split == 2 ? 76 : split == 4 ? 36 : 15; }
+
+// How many CTAs share a gate/up unit, by the rounds of units and a unit's time:
+// an SM takes a K block in 0.42 us, a join 1.5 us.  Measured (calls; 1, 2, 4, 8 CTAs):
+// 4 units of 56 K blocks 33, 23, 16, 13 us; 30 of 56: 39, 28, 23, 26; 64 of 56: 43,
+// 34, 37, 46; 88 of 22: 29, 35, 35, 45; 128 of 8: 14, 18, 20, 31.
+int gateup_split(int64_t units, int hb) {
+  int best = 1;
+  int64_t cost = (units + clusters_of(1) - 1) / clusters_of(1) * hb * 42;  // 10 ns
+  for (int s = 2; s <= 8; s *= 2) {
+    const int64_t c = (units + clusters_of(s) - 1) / clusters_of(s) * ((hb + 2 * s - 1) / (2 * s) * 84 + 150);
+    if (c < cost) cost = c, best = s;
+  }
+  return best;
 }
 
 // One CTA: 16 output columns (rows of every chosen expert's W2), all tokens.
@@ -331,8 +394,18 @@ cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weig
   p.T = d.T, p.H = d.H, p.I = d.I, p.E = d.E, p.k = d.top_k, p.shared = d.n_shared;
   // one CTA fills an SM's registers; its units follow each other
   const int64_t units = list_cap(d) * (d.I / kBlk);
-  const cudaError_t e = launch_pdl(experts_gateup_kernel, dim3((unsigned)std::min<int64_t>(units, sms)), dim3(kGuThreads),
-                                   0, s, p);
+  p.split = gateup_split(units, d.H / kBlk);
+  cudaError_t e;
+  if (p.split > 1) {
+    const int64_t n = std::min(units, clusters_of(p.split));
+    const size_t smem = (size_t)(p.split - 1) * 8 * 8 * 32 * sizeof(float);
+    e = cudaFuncSetAttribute(experts_gateup_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 7 * 8192);
+    if (e == cudaSuccess)
+      e = launch_pdl_cluster(experts_gateup_kernel<true>, dim3((unsigned)(n * p.split)), dim3(kGuThreads), smem, s,
+                             (unsigned)p.split, p);
+  } else {
+    e = launch_pdl(experts_gateup_kernel<false>, dim3((unsigned)std::min<int64_t>(units, sms)), dim3(kGuThreads), 0, s, p);
+  }
   if (e != cudaSuccess) return e;
   // an SM runs 24 warps of the down kernel: as one CTA where the output columns
   // make at most two a SM (8 tokens, H = 1024, I = 512, 32 experts: 14 us a call
