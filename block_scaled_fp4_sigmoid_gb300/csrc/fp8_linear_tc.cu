@@ -12,8 +12,8 @@
 // What bounds it: shared memory.  A K block of a 128 x 256 tile writes 48 KB of
 // operands there and the MMAs read them again, 768 cycles at 128 bytes a cycle
 // against 512 of the tensor core (fp8); measured 780 without the epilogue's
-// sums, 840 with them (16384 x 7168 x 7168 in 593 us, 2.84 PFLOP/s).  Run for
-// seconds the board's power cap takes the clock to 1.6 GHz: 680 us.  CTA pairs
+// sums, 840 with them (16384 x 7168 x 7168 in 583 us, 2.89 PFLOP/s).  Run for
+// seconds the board's power cap takes the clock to 1.6 GHz: 670 us.  CTA pairs
 // (256 x 256 over two SMs, 512 cycles of shared memory) reached 474 us without
 // the sums but 615 with them: two buffers of tensor memory are then too few for
 // the way round over both CTAs.  Operands multicast to two CTAs changed nothing.
