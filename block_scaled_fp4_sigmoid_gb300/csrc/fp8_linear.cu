@@ -17,6 +17,7 @@ struct StreamParams {
   int64_t out_ld;
   int32_t* status;  // nullable; cleared here (this kernel waits for nothing)
   int T, K, N, out_fp32;
+  int ahead;  // fetch weights ahead of the wait
 };
 
 constexpr int kStreamWarps = 8;
@@ -25,10 +26,21 @@ constexpr int kStreamWarps = 8;
 // RUN 128-column blocks in turn, all loads of a run issued together, straight
 // from global memory into mma.sync operands (every weight byte once, 16 per
 // lane), and their sums are joined in warp order.  HBM bound: 8 tokens and 7168
-// x 36864 weights in 44 us, 6.0 TB/s.
+// x 36864 weights in 42 us, 6.3 TB/s.
+//
+// Weights fetched into L2 before the wait for the launch before: 44.1 -> 42.0 us, 4
+// x 4096 x 4096 4.8 -> 3.9, 16 x 7168 x 2112 6.8 -> 6.3; for up to 8 tokens and a CTA an
+// SM at most it does not pay (1 x 7168 x 2112 4.0 -> 4.3).  Fetched ahead inside the
+// loop too: 53 to 63 us.
 template <int NT, int MIN_CTAS, int RUN>
 __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_kernel(const StreamParams p) {
   __shared__ float part[kStreamWarps][NT * 4][32];
+  {
+    // the first run's weights on their way into L2 while the launch before ends
+    const int row = min((int)blockIdx.x * 16 + ((int)threadIdx.x & 15), p.N - 1), b = ((int)threadIdx.x >> 5) * RUN;
+    const int n = min(RUN * kBlk, p.K - b * kBlk);
+    if (p.ahead && (threadIdx.x & 31) < 16 && n > 0) prefetch_l2(p.w + (int64_t)row * p.K + b * kBlk, n);
+  }
   pdl_wait();
   pdl_trigger();
   if (p.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kStatusInts) p.status[threadIdx.x] = 0;
@@ -107,9 +119,9 @@ size_t linear_fp8_workspace(int, int, int) { return 256; }
 // former starts 1 to 2 us sooner, the latter has no rounds of CTAs each with
 // a latency of its own, and reads the weights once where the former reads them for
 // every 16 tokens.  Up to 128 tokens the smaller of two estimates decides, both
-// fitted to measurements (stream, tensor cores): 8 x 7168 x 36864 44.0, 44.5 us;
-// 8 x 1024 x 131072 36.7, 26.8; 16 x 7168 x 36864 74.7, 44.8; 16 x 7168 x 2112 6.8,
-// 7.9; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  In 10 ns:
+// fitted to measurements (stream, tensor cores): 8 x 7168 x 36864 42.0, 42.4 us;
+// 8 x 1024 x 131072 36.7, 26.8; 16 x 7168 x 36864 74.7, 42.1; 16 x 7168 x 2112 6.3,
+// 7.8; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  In 10 ns:
 static int64_t stream_cost(const LinearFp8Args& a) {
   const int64_t sms = 152, nb = blocks128(a.K), ctas = (a.N + 15) / 16 * (a.T > 8 ? (a.T + 15) / 16 : 1);
   const int64_t rounds = (ctas + 3 * sms - 1) / (3 * sms);  // of three CTAs an SM
@@ -121,7 +133,7 @@ static int64_t stream_cost(const LinearFp8Args& a) {
 // flight a warp.  With row tiles for all of them, two blocks a run and three CTAs
 // an SM stream best, unless the last round of CTAs would be much emptier than
 // with one block and four CTAs (7168 x 7168, 448 tiles, 8 tokens: 11.0 us against
-// 11.9; 7168 x 36864, 2304 tiles: 49.6 against 43.9).  Where the tiles hardly
+// 11.9; 7168 x 36864, 2304 tiles: 49.6 against 44.1).  Where the tiles hardly
 // cover the SMs, four blocks a run (7168 x 2112, 132 tiles: 4.4 us against 5.2;
 // 16 tokens 6.9 against 10.1).
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
@@ -131,7 +143,7 @@ cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
   const int64_t stream = stream_cost(a) - 250;  // (what the tensor cores start later)
   if (stream > (int64_t)a.K * a.N / 56000 && stream > linear_fp8_tc_cost(a.T, a.K, a.N)) return launch_linear_fp8_tc(a, s);
   const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
-                       a.out_fp32 ? 1 : 0};
+                       a.out_fp32 ? 1 : 0, a.T > 8 || ctas > sms};
   const dim3 grid((unsigned)rows, (unsigned)chunks), block(32 * kStreamWarps);
   if (a.T > 8) {
     if (ctas <= sms) return launch_pdl(linear_stream_kernel<2, 1, 4>, grid, block, 0, s, p);

@@ -112,6 +112,11 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(s));
 }
 
+// The box of a 2-D tensor map at (x, y) on its way into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
+}
+
 // The two halves of cluster_arrive_wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -332,6 +337,12 @@ __global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kerne
     prefetch_tmap(&p.tmw);
     prefetch_tmap(&p.tmx1);
     prefetch_tmap(&p.tmw1);
+    // One token tile: the first weight boxes on their way into L2 while the launch
+    // before ends (16 x 7168 x 36864 43.6 -> 42.1 us; with more token tiles no gain).
+    if (p.plan.mtiles == 1 && first < tiles) {
+      const CUtensorMap* tmw = first + 1 == tiles ? &p.tmw1 : &p.tmw;
+      for (int kb = kb0; kb < min(kb1, kb0 + 3); ++kb) tma_prefetch_2d(tmw, kb * 128, first * BN);
+    }
   }
   // The second launch of a call begins once every CTA of the first has passed
   // its own wait, so its inputs are complete; it waits for the first at its end,

@@ -223,7 +223,8 @@ def test_linear_into_aligned_columns_of_a_wider_output(ops, T, K, N, fp32):
 @pytest.mark.parametrize("fp32", [False, True])
 @pytest.mark.parametrize("at", [0, 1, 6])
 @pytest.mark.parametrize("T,K,N", [(40, 14336, 291), (130, 2048, 811), (257, 4096, 1501), (200, 4096, 4099), (163, 576, 2925),
-                                   (9, 1024, 8191), (600, 512, 5001), (70, 2048, 1029)])
+                                   (9, 1024, 8191), (600, 512, 5001), (70, 2048, 1029),
+                                   (5, 512, 24571)])
 def test_linear_rows_that_start_anywhere(ops, T, K, N, at, fp32):
     """Odd widths, first columns off 16 bytes, few rows in the last tile: tiles of one CTA and of
     clusters of two, four and eight, against 64 bits; nothing else is written."""
