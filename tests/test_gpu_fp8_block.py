@@ -461,3 +461,25 @@ def test_refusals_on_tensors(ops):
     with pytest.raises(fm.Fp4MoeError) as e:
         ops.experts_fp8_block(*[dev(v) for v in (xq, xs, idx, wts, *w)])  # more than 16 tokens
     assert e.value.code == fm.STATUS_CODE["FP4MOE_ERR_UNSUPPORTED_SHAPE"]
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 4096, 128, 4, 1), (4, 4096, 512, 16, 4), (8, 512, 256, 32, 4)])
+def test_experts_calls_in_a_row_on_one_workspace(ops, T, H, I, E, k):
+    """Each call starts while the one before it ends and both use one workspace: the same outputs
+    as calls that wait (units of a CTA of their own, and shared by clusters)."""
+    import torch
+    xq, xs, idx, wts, w, _ = expert_inputs(T, H, I, E, k, 21)
+    wd = [dev(v) for v in w]
+    calls = [[dev(v) for v in (np.roll(xq, 128 * i, 1), xs, (idx + i) % E, wts + i)] for i in range(6)]
+    ws = torch.empty(fm.experts_fp8_block_workspace_size(fm.make_dims(T, H, I, E, k, fmt=fm.FP8)), dtype=torch.uint8,
+                     device="cuda")
+    want = []
+    for a in calls:
+        want.append(ops.experts_fp8_block(*a, *wd, ws=ws))
+        torch.cuda.synchronize()
+    got = [torch.empty_like(v) for v in want]
+    for _ in range(20):
+        for a, o in zip(calls, got):
+            ops.experts_fp8_block(*a, *wd, out=o, ws=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
