@@ -28,7 +28,8 @@ struct ExpertsParams {
   float* hs;     // [entry * 8 + column, I / 128]
   uint16_t* out;
   int T, H, I, E, k, shared;
-  int split;  // CTAs that share a gate/up unit
+  int split;   // CTAs that share a gate/up unit
+  int dsplit;  // CTAs that share 16 output columns
 };
 
 struct ExpertList {
@@ -257,7 +258,8 @@ int gateup_split(int64_t units, int hb) {
 // One CTA: 16 output columns (rows of every chosen expert's W2), all tokens.
 // Runs of two K blocks go to the warps in turn, over all entries; a warp adds
 // weight * scales * product to its token columns, and the warps' sums are
-// joined in warp order, so the result does not depend on timing.  A warp's sums
+// joined in warp order, so the result does not depend on timing (SPLIT: a cluster's
+// CTAs share the runs, and CTA 0 joins their sums in its order).  A warp's sums
 // are in registers where column = token (T <= 8), else in its own shared memory
 // (GATHER).
 //
@@ -270,11 +272,14 @@ int gateup_split(int64_t units, int hb) {
 // The gate/up kernel has passed its own wait before this one can start, so all
 // but its output (h) is complete: the list and the routing weights are made
 // before the wait.
-template <bool GATHER, int kDnWarps>
+template <bool GATHER, int kDnWarps, bool SPLIT>
 __global__ void __launch_bounds__(32 * kDnWarps, 24 / kDnWarps) experts_down_kernel(const ExpertsParams p) {
   __shared__ ExpertList L;
   __shared__ float rw[kMaxList][8];  // routing weight of (entry, column)
   __shared__ float sums[kDnWarps][16][GATHER ? 17 : 9];  // row, token
+  __shared__ float others[SPLIT ? 3 : 1][16 * kMaxTok];  // SPLIT: the other CTAs' sums
+  const int S = SPLIT ? p.dsplit : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
+  if constexpr (SPLIT) cluster_arrive();
   list_experts(p, L);
   for (int o = threadIdx.x; o < L.n * 8; o += blockDim.x) {
     const int u = o >> 3, tok = L.tok[u][o & 7], e = L.e[u];
@@ -291,16 +296,16 @@ __global__ void __launch_bounds__(32 * kDnWarps, 24 / kDnWarps) experts_down_ker
   if constexpr (GATHER)
     for (int o = lane; o < 16 * 17; o += 32) sums[warp][0][o] = 0.f;
   __syncthreads();
-  const int n0 = blockIdx.x * 16, hb = p.H / kBlk, ib = p.I / kBlk;
+  const int n0 = (int)blockIdx.x / S * 16, hb = p.H / kBlk, ib = p.I / kBlk;
   const int64_t wat = (int64_t)(n0 + g) * p.I + 16 * t, sat = (int64_t)(n0 / kBlk) * ib;  // into an expert's weights, scales
   constexpr int kRun = 2;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  // a warp takes every kDnWarps-th run of kRun K blocks, over all entries
+  // a warp takes every S kDnWarps-th run of kRun K blocks, over all entries
   const int runs = (ib + kRun - 1) / kRun;
-  int u = 0, r = warp;
+  int u = 0, r = rank * kDnWarps + warp;
   pdl_wait();
   pdl_trigger();
-  for (;; r += kDnWarps) {
+  for (;; r += S * kDnWarps) {
     while (r >= runs) r -= runs, ++u;
     if (u >= L.n) break;
     const int e = L.e[u], b0 = r * kRun;
@@ -357,6 +362,25 @@ __global__ void __launch_bounds__(32 * kDnWarps, 24 / kDnWarps) experts_down_ker
     sums[warp][g + 8][2 * t] = acc[2], sums[warp][g + 8][2 * t + 1] = acc[3];
   }
   __syncthreads();
+  if constexpr (SPLIT) {
+    static_assert(32 * kDnWarps >= 16 * kMaxTok, "an output a thread");
+    const int o = threadIdx.x, tok = o >> 4, row = o & 15;
+    float v = 0.f;
+    if (o < 16 * p.T) {
+#pragma unroll
+      for (int wq = 0; wq < kDnWarps; ++wq) v += sums[wq][row][tok];
+    }
+    __syncwarp();
+    cluster_wait();  // every CTA has begun
+    if (rank > 0 && o < 16 * p.T) st_cluster(smem_u32(&others[rank - 1][o]), 0, v);
+    __syncwarp();
+    cluster_arrive_wait();
+    if (rank == 0 && o < 16 * p.T) {
+      for (int q = 0; q < S - 1; ++q) v += others[q][o];
+      p.out[(int64_t)tok * p.H + n0 + row] = f32_to_bf16_rn(v);
+    }
+    return;
+  }
   for (int o = threadIdx.x; o < 16 * p.T; o += 32 * kDnWarps) {
     const int tok = o >> 4, r = o & 15;
     float v = 0.f;
@@ -364,6 +388,21 @@ __global__ void __launch_bounds__(32 * kDnWarps, 24 / kDnWarps) experts_down_ker
     for (int wq = 0; wq < kDnWarps; ++wq) v += sums[wq][r][tok];
     p.out[(int64_t)tok * p.H + n0 + r] = f32_to_bf16_rn(v);
   }
+}
+
+// How many CTAs share 16 output columns of the down kernel, by the K blocks over all
+// entries and the number of such column groups.  24 warps take 48 K blocks in about
+// 1 us, a join 1.5 us (two CTAs) or 2.2 (four).  Measured (calls; 1, 2, 4 CTAs): 16
+// tokens, 76 entries, H 256, I 2048 53, 39, 33 us; H 512, I 512 22, 19, 20; H 1024, I
+// 2048 76, 64 us; 4 tokens, 16 entries, H 512, I 2048 21, 19, 18; I 512 9, 10, 12.
+int down_split(int64_t blocks, int64_t cols) {
+  int best = 1;
+  int64_t cost = blocks * 100 / 48;  // 10 ns
+  for (int s = 2; s <= 4; s *= 2) {
+    const int64_t c = blocks * 100 / (48 * s) + (s == 2 ? 150 : 220);
+    if (cols <= clusters_of(s) && c < cost) cost = c, best = s;
+  }
+  return best;
 }
 
 // Entries of the list: an expert with c tokens has ceil(c / 8) <= 1 + c / 8.
@@ -407,13 +446,19 @@ cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weig
     e = launch_pdl(experts_gateup_kernel<false>, dim3((unsigned)std::min<int64_t>(units, sms)), dim3(kGuThreads), 0, s, p);
   }
   if (e != cudaSuccess) return e;
+  p.dsplit = down_split(list_cap(d) * (d.I / kBlk), d.H / 16);
+  const unsigned cols = (unsigned)(d.H / 16);
+  if (p.dsplit > 1)
+    return launch_pdl_cluster(d.T <= 8 ? experts_down_kernel<false, 24, true> : experts_down_kernel<true, 24, true>,
+                              dim3(cols * p.dsplit), dim3(768), 0, s, (unsigned)p.dsplit, p);
   // an SM runs 24 warps of the down kernel: as one CTA where the output columns
   // make at most two a SM (8 tokens, H = 1024, I = 512, 32 experts: 14 us a call
   // against 20), else as three (one token, H = 7168: 68 us against 75)
-  const dim3 grid(d.H / 16);
-  if (d.H / 16 <= 2 * sms)
-    return launch_pdl(d.T <= 8 ? experts_down_kernel<false, 24> : experts_down_kernel<true, 24>, grid, dim3(768), 0, s, p);
-  return launch_pdl(d.T <= 8 ? experts_down_kernel<false, 8> : experts_down_kernel<true, 8>, grid, dim3(256), 0, s, p);
+  if (cols <= 2u * sms)
+    return launch_pdl(d.T <= 8 ? experts_down_kernel<false, 24, false> : experts_down_kernel<true, 24, false>, dim3(cols),
+                      dim3(768), 0, s, p);
+  return launch_pdl(d.T <= 8 ? experts_down_kernel<false, 8, false> : experts_down_kernel<true, 8, false>, dim3(cols),
+                    dim3(256), 0, s, p);
 }
 
 }  // namespace fp4moe

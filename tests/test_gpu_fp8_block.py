@@ -321,7 +321,9 @@ EXPERTS = [dict(T=1, H=256, I=128, E=4, k=1), dict(T=1, H=1024, I=384, E=16, k=8
            dict(T=3, H=5120, I=128, E=4, k=2), dict(T=12, H=5120, I=384, E=5, k=3, shared=True),
            # gate/up units shared by eight, four and two CTAs, and by two in several rounds
            dict(T=1, H=4096, I=128, E=4, k=1), dict(T=3, H=2048, I=384, E=6, k=2), dict(T=4, H=4096, I=512, E=16, k=4),
-           dict(T=2, H=2304, I=256, E=3, k=2, shared=True), dict(T=16, H=5120, I=640, E=12, k=12)]
+           dict(T=2, H=2304, I=256, E=3, k=2, shared=True), dict(T=16, H=5120, I=640, E=12, k=12),
+           # output columns shared by four and two CTAs
+           dict(T=7, H=512, I=1024, E=24, k=6, shared=True), dict(T=16, H=1024, I=768, E=24, k=6, outside=0.3)]
 
 
 @pytest.mark.parametrize("c", EXPERTS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
