@@ -2,7 +2,9 @@
 token and 128 columns (activations) or per 128 x 128 block (weights).
 
 The functions check their tensors, allocate what the caller does not pass and
-call the library on the current stream of the tensors' device.  (Each check is
+call the library on the current stream of the tensors' device, with that device
+current for the call: the library launches on the thread's current device, and
+the default stream's handle is the same number on every device.  (Each check is
 one expression over all tensors, a few microseconds less than one call a
 tensor; what is wrong is worked out only once something is.)  Codes are
 torch.uint8 or torch.float8_e4m3fn tensors.  ``Fp8BlockMlp`` and
@@ -59,6 +61,7 @@ def _device(t):
 # the raw handle of a device's current stream, without a Stream object around it
 _stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None, q=None, scales=None,
@@ -72,6 +75,9 @@ def add_rmsnorm_fp8(x, residual, gamma, eps: float, *, residual_out=None, y=None
     shape = x.shape
     T, H = shape
     dev = _device(x)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return add_rmsnorm_fp8(x, residual, gamma, eps, residual_out=residual_out, y=y, q=q, scales=scales, want_y=want_y)
     if residual is not None and residual_out is None:
         residual_out = torch.empty(shape, dtype=_bf16, device=x.device)
     if y is None and want_y:
@@ -111,6 +117,9 @@ def swiglu_fp8(gu, *, q=None, scales=None):
     T, I = gu.shape
     I //= 2
     dev = _device(gu)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_fp8(gu, q=q, scales=scales)
     if q is None:
         q = torch.empty((T, I), dtype=torch.uint8, device=gu.device)
     if scales is None:
@@ -137,6 +146,9 @@ def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, 
     (T, K), N = xq.shape, w.shape[0]
     kb = (K + 127) // 128
     dev = _device(xq)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return linear_fp8_block(xq, xs, w, w_scale, out=out, out_dtype=out_dtype, ws=ws)
     if out is None:
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype: bf16 or fp32, got {out_dtype}")
@@ -169,6 +181,10 @@ def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh
                          f"{tuple(topk_idx.shape)}, {tuple(w13.shape)}")
     (T, H), k, E, I = xq.shape, topk_idx.shape[1], w13.shape[0], w13.shape[1] // 2
     dev = _device(xq)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh13, sh13_scale, sh2,
+                                     sh2_scale, out=out, ws=ws)
     _check("xq", xq, (T, H), _CODES, dev)
     _check("xs", xs, (T, _blocks(H)), _F32, dev)
     _check("topk_idx", topk_idx, (T, k), (torch.int32,), dev)
@@ -236,6 +252,9 @@ class Fp8BlockMoE:
         """(topk_idx, topk_w) of the bf16 rows y [T, H]."""
         d = self.dims
         dev = _device(y)
+        if _current_device() != dev:
+            with torch.cuda.device(dev):
+                return self.route(y)
         _check("y", y, (d.T, d.H), _BF16, dev)
         idx = torch.empty((d.T, d.top_k), dtype=torch.int32, device=self.device)
         w = torch.empty((d.T, d.top_k), dtype=torch.float32, device=self.device)

@@ -1,0 +1,93 @@
+"""The tensor functions of the block-scaled FP8 operators up to the launch, on
+CPU tensors: the library calls are replaced by recorders and the device index
+of CPU tensors (-1) stands for a GPU other than the current one."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from block_scaled_fp4_sigmoid_gb300 import build  # noqa: E402
+
+CALLS = ("_add_rmsnorm", "_swiglu", "_linear", "_experts", "_route")
+
+
+class Launches:
+    """What would have been launched: the call's name, its arguments and the current device."""
+
+    def __init__(self, current):
+        self.current, self.seen = current, []
+
+    def record(self, name):
+        return lambda *args: self.seen.append((name, args, self.current))
+
+
+@pytest.fixture
+def fb(monkeypatch):
+    build.build_library()
+    from block_scaled_fp4_sigmoid_gb300 import fp8_block
+    monkeypatch.setattr(fp8_block, "_device", lambda t: t.get_device())
+    monkeypatch.setattr(fp8_block, "_stream", lambda device: 1000 + device)
+    return fp8_block
+
+
+@pytest.fixture
+def launches(fb, monkeypatch):
+    """Current device 0; torch.cuda.device(d) makes d current while it lasts."""
+    rec = Launches(0)
+
+    class device:
+        def __init__(self, d):
+            self.d = d if isinstance(d, int) else d.index
+
+        def __enter__(self):
+            self.before, rec.current = rec.current, self.d
+
+        def __exit__(self, *exc):
+            rec.current = self.before
+
+    monkeypatch.setattr(fb, "_current_device", lambda: rec.current, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: rec.current)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for name in CALLS:
+        monkeypatch.setattr(fb, name, rec.record(name))
+    return rec
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def f32(*shape):
+    return torch.zeros(shape)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def expert_args(T=2, H=256, I=128, E=4, k=2):
+    return [u8(T, H), f32(T, H // 128), torch.zeros((T, k), dtype=torch.int32), f32(T, k), u8(E, 2 * I, H),
+            f32(E, 2 * I // 128, H // 128), u8(E, H, I), f32(E, H // 128, I // 128)]
+
+
+def linear_args(T=4, K=256, N=128):
+    return [u8(T, K), f32(T, K // 128), u8(N, K), f32(-(-N // 128), K // 128)]
+
+
+def call_all(fb):
+    fb.add_rmsnorm_fp8(bf16(3, 256), None, bf16(256), 1e-6)
+    fb.swiglu_fp8(bf16(3, 512))
+    fb.linear_fp8_block(*linear_args())
+    fb.experts_fp8_block(*expert_args(), out=bf16(2, 256))
+
+
+@pytest.mark.parametrize("current", [0, -1])
+def test_every_launch_has_its_tensors_device_current(fb, launches, current):
+    """A launch goes to the current device, and the default stream's handle is the same number on
+    every device: with the tensors' device not current it would run elsewhere on their addresses."""
+    launches.current = current
+    call_all(fb)
+    assert [n for n, _, _ in launches.seen] == ["_add_rmsnorm", "_swiglu", "_linear", "_experts"]
+    for name, args, device in launches.seen:
+        assert device == -1, name
+        assert args[-1] == 999, name  # the stream of that device
+    assert launches.current == current
