@@ -251,7 +251,7 @@ class Fp8BlockMoE:
     def route(self, y):
         """(topk_idx, topk_w) of the bf16 rows y [T, H]."""
         d = self.dims
-        dev = _device(y)
+        dev = _device(self.w_router)
         if _current_device() != dev:
             with torch.cuda.device(dev):
                 return self.route(y)

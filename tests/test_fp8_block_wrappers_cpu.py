@@ -91,3 +91,24 @@ def test_every_launch_has_its_tensors_device_current(fb, launches, current):
         assert device == -1, name
         assert args[-1] == 999, name  # the stream of that device
     assert launches.current == current
+
+
+def moe(fb, T=2, H=256, I=128, E=4, k=2, **kw):
+    import block_scaled_fp4_sigmoid_gb300 as fm
+    dims = fm.make_dims(T, H, I, E, k, fmt=fm.FP8)
+    return fb.Fp8BlockMoE(dims, bf16(H), bf16(E, H), f32(E), *expert_args(T, H, I, E, k)[4:], **kw)
+
+
+def test_the_router_refuses_rows_of_another_device_than_its_weights(fb, launches, monkeypatch):
+    layer = moe(fb)
+    y = bf16(2, 256)
+    assert layer.route(y)[0].shape == (2, 2)
+
+    class Elsewhere:
+        """y as a tensor of device 3."""
+        shape, dtype, device = y.shape, y.dtype, "cuda:3"
+        get_device, is_contiguous, data_ptr = (lambda self: 3), (lambda self: True), (lambda self: 64)
+
+    with pytest.raises(ValueError, match="y: "):
+        layer.route(Elsewhere())
+    assert len(launches.seen) == 1
