@@ -51,6 +51,13 @@ def _out(name, t, shape, dtypes, device, dense=True):
     return t
 
 
+def _check_ws(ws, device):
+    """A workspace: its bytes are all there, on the device."""
+    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: dense uint8 on cuda:{device} expected, got {tuple(ws.shape)} of {ws.dtype} on {ws.device} with "
+                         f"strides {ws.stride()}")
+
+
 def _device(t):
     d = t.get_device()
     if d < 0:
@@ -138,7 +145,7 @@ def swiglu_fp8(gu, *, q=None, scales=None):
 def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, ws=None):
     """out [T, N] = x . W^T for codes xq [T, K] with scales xs [T, K/128] and w [N, K] with
     w_scale [N/128, K/128] (fp4moe_linear_fp8_block; blocks rounded up).  out: bf16 or fp32,
-    rows may be strided.  ws: None, or a uint8 tensor of linear_fp8_block_workspace_size(T, K, N)
+    rows may be strided.  ws: None, or a dense uint8 tensor of linear_fp8_block_workspace_size(T, K, N)
     bytes whose status word get_status reads; without it a device-side timeout is recorded in
     the library's word, which linear_fp8_block_status reads."""
     if xq.dim() != 2 or w.dim() != 2:
@@ -163,6 +170,8 @@ def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, 
         _check("w", w, (N, K), _CODES, dev)
         _check("w_scale", w_scale, (_blocks(N), kb), _F32, dev)
         _check("out", out, (T, N), _OUT, dev, dense=False)
+    if ws is not None:
+        _check_ws(ws, dev)
     if T:
         _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
                 out.stride(0) if T > 1 else N, out.dtype is _f32, None if ws is None else ws.data_ptr(),
@@ -175,7 +184,8 @@ def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh
     """bf16 [T, H]: the routed experts of up to 16 tokens, plus the shared one where given
     (fp4moe_experts_fp8_block).  xq [T, H], xs [T, H/128]; topk_idx int32 and topk_w fp32 [T, k]
     (an index outside [0, E) is skipped); w13 [E, 2I, H], w2 [E, H, I] with one scale per 128 x
-    128 block."""
+    128 block.  ws: None, or a dense uint8 tensor of experts_fp8_block_workspace_size bytes that no
+    call on another stream uses meanwhile."""
     if xq.dim() != 2 or topk_idx.dim() != 2 or w13.dim() != 3:
         raise ValueError(f"xq, topk_idx, w13: two, two and three dimensions expected, got {tuple(xq.shape)}, "
                          f"{tuple(topk_idx.shape)}, {tuple(w13.shape)}")
@@ -204,6 +214,8 @@ def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh
     out = _out("out", out, (T, H), _BF16, dev)
     if ws is None:
         ws = torch.empty(n, dtype=torch.uint8, device=xq.device)
+    else:
+        _check_ws(ws, dev)
     weights = Fp8BlockWeights(w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), _ptr(sh13),
                               _ptr(sh13_scale), _ptr(sh2), _ptr(sh2_scale))
     _experts(dims, weights, xq.data_ptr(), xs.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(),

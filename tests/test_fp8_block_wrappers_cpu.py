@@ -112,3 +112,38 @@ def test_the_router_refuses_rows_of_another_device_than_its_weights(fb, launches
     with pytest.raises(ValueError, match="y: "):
         layer.route(Elsewhere())
     assert len(launches.seen) == 1
+
+
+class OnHost:
+    """A CPU workspace, for calls whose tensors' device (-1 here) would be a GPU."""
+    dtype, shape = torch.uint8, torch.Size([1 << 20])
+    get_device, is_contiguous, data_ptr = (lambda self: -2), (lambda self: True), (lambda self: 64)
+    device, stride, numel, dim = "cpu", (lambda self: (1,)), (lambda self: 1 << 20), (lambda self: 1)
+
+
+BAD_WORKSPACES = {
+    "on another device": lambda: OnHost(),
+    "expanded from one byte": lambda: u8(1).expand(1 << 20),
+    "every second byte": lambda: u8(1 << 20)[::2],
+    "of another type": lambda: torch.zeros(1 << 20, dtype=torch.int32),
+}
+
+
+@pytest.mark.parametrize("kind", BAD_WORKSPACES)
+def test_workspaces_that_do_not_hold_their_bytes_are_refused(fb, launches, kind):
+    """The kernels write to the workspace: one on the host, or with fewer bytes behind it than it
+    counts, is written past its end."""
+    ws = BAD_WORKSPACES[kind]()
+    with pytest.raises(ValueError, match="ws: "):
+        fb.linear_fp8_block(*linear_args(), ws=ws)
+    with pytest.raises(ValueError, match="ws: "):
+        fb.experts_fp8_block(*expert_args(), out=bf16(2, 256), ws=ws)
+    assert not launches.seen
+
+
+def test_workspaces_of_any_shape_are_taken(fb, launches):
+    for ws in (u8(1 << 16), u8(256, 256), u8(1 << 17)[256:]):
+        fb.linear_fp8_block(*linear_args(), ws=ws)
+        fb.experts_fp8_block(*expert_args(), out=bf16(2, 256), ws=ws)
+        for name, args, _ in launches.seen[-2:]:
+            assert args[-3:-1] == (ws.data_ptr(), ws.numel()), name
