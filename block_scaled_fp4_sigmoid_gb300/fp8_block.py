@@ -245,7 +245,9 @@ class Fp8BlockMoE:
     """A mixture-of-experts feed-forward sublayer for up to 16 tokens: norm ->
     router (fp4moe_route on the bf16 norm output) -> experts (and the shared
     one) on block-scaled FP8 weights.  dims: as make_dims returns for the
-    layer with fmt=FP8; w_router bf16 [E, H], bias fp32 [E]."""
+    layer with fmt=FP8; w_router bf16 [E, H], bias fp32 [E].  The object keeps
+    its weights only: each call's scratch comes from the allocator, so calls on
+    several streams do not meet."""
 
     def __init__(self, dims: Dims, gamma, w_router, bias, w13, w13_scale, w2, w2_scale, sh13=None, sh13_scale=None,
                  sh2=None, sh2_scale=None, eps: float = 1e-6):
@@ -256,26 +258,34 @@ class Fp8BlockMoE:
         self.device = w13.device
         _check("w_router", w_router, (dims.E, dims.H), _BF16, _device(w13))
         _check("bias", bias, (dims.E,), _F32, _device(w13))
-        self.ws_bytes = workspace_size(dims)  # of the router
-        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
-        self.experts_ws = torch.empty(experts_fp8_block_workspace_size(dims), dtype=torch.uint8, device=self.device)
+        # the router's, then the experts'
+        self.ws_bytes = max(workspace_size(dims), experts_fp8_block_workspace_size(dims))
 
-    def route(self, y):
-        """(topk_idx, topk_w) of the bf16 rows y [T, H]."""
+    def _scratch(self):
+        return torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def route(self, y, ws=None):
+        """(topk_idx, topk_w) of the bf16 rows y [T, H].  ws: None, or a dense uint8 tensor of
+        self.ws_bytes bytes."""
         d = self.dims
         dev = _device(self.w_router)
         if _current_device() != dev:
             with torch.cuda.device(dev):
-                return self.route(y)
+                return self.route(y, ws)
         _check("y", y, (d.T, d.H), _BF16, dev)
         idx = torch.empty((d.T, d.top_k), dtype=torch.int32, device=self.device)
         w = torch.empty((d.T, d.top_k), dtype=torch.float32, device=self.device)
+        if ws is None:
+            ws = self._scratch()
+        else:
+            _check_ws(ws, dev)
         _route(d, y.data_ptr(), self.w_router.data_ptr(), self.bias.data_ptr(), idx.data_ptr(), w.data_ptr(), None,
-               self.ws.data_ptr(), self.ws_bytes, _stream(dev))
+               ws.data_ptr(), ws.numel(), _stream(dev))
         return idx, w
 
     def forward(self, x, residual=None):
         """As Fp8BlockMlp.forward."""
         res, y, q, s = add_rmsnorm_fp8(x, residual, self.gamma, self.eps, want_y=True)
-        idx, w = self.route(y)
-        return experts_fp8_block(q, s, idx, w, *self.weights, ws=self.experts_ws), res
+        ws = self._scratch()
+        idx, w = self.route(y, ws)
+        return experts_fp8_block(q, s, idx, w, *self.weights, ws=ws), res

@@ -147,3 +147,19 @@ def test_workspaces_of_any_shape_are_taken(fb, launches):
         fb.experts_fp8_block(*expert_args(), out=bf16(2, 256), ws=ws)
         for name, args, _ in launches.seen[-2:]:
             assert args[-3:-1] == (ws.data_ptr(), ws.numel()), name
+
+
+def test_a_layer_object_keeps_nothing_that_its_calls_write(fb, launches, monkeypatch):
+    """Two streams may call one layer: each call's scratch is its own, from the allocator."""
+    monkeypatch.setattr(fb, "_out", lambda name, t, shape, dtypes, device: torch.empty(shape, dtype=dtypes[0]))
+    layer = moe(fb)
+    layer.forward(bf16(2, 256))
+    kept = [t for v in vars(layer).values() for t in (v if isinstance(v, tuple) else [v]) if torch.is_tensor(t)]
+    weights = [layer.gamma, layer.w_router, layer.bias, *layer.weights]
+    scratch = [a[-3] for n, a, _ in launches.seen if n in ("_route", "_experts")]
+    assert len(scratch) == 2
+    for t in kept:
+        inside = [p for p in scratch if t.data_ptr() <= p < t.data_ptr() + t.numel() * t.element_size()]
+        assert not inside or any(t is w for w in weights)
+    with pytest.raises(Exception, match="UNSUPPORTED|unsupported"):
+        moe(fb, T=17)  # refused when the layer is made, as before
