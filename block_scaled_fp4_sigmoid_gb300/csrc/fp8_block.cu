@@ -204,6 +204,11 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 constexpr int32_t kMaxRows = 1 << 20;  // rows of one call
 constexpr int32_t kMaxCols = 65536;
+bool experts_sizes_ok(const fp4moe_dims& d) {
+  return d.T >= 1 && d.T <= kExpertsMaxT && d.H >= kBlk && d.H <= kMaxCols && d.H % kBlk == 0 && d.I >= kBlk &&
+         d.I <= kMaxCols && d.I % kBlk == 0 && d.E >= 1 && d.E <= kExpertsMaxE && d.top_k >= 1 &&
+         d.top_k <= kExpertsMaxK && (d.n_shared == 0 || d.n_shared == 1);
+}
 }  // namespace
 
 extern "C" {
@@ -264,8 +269,7 @@ fp4moe_status fp4moe_linear_fp8_block_status(void* stream, fp4moe_status* st, in
 }
 
 size_t fp4moe_experts_fp8_block_workspace_size(const fp4moe_dims* dims) {
-  Layout L;
-  if (!dims || dims->fmt != FP4MOE_FP8 || dims->T > kExpertsMaxT || !make_layout(*dims, &L)) return 0;
+  if (!dims || dims->fmt != FP4MOE_FP8 || !experts_sizes_ok(*dims)) return 0;
   return experts_fp8_workspace(*dims);
 }
 

@@ -15,7 +15,7 @@ namespace fp4moe {
 
 namespace {
 
-constexpr int kMaxE = 512, kMaxTok = kExpertsMaxT, kMaxRoutes = 16 * kMaxTok;
+constexpr int kMaxE = kExpertsMaxE, kMaxTok = kExpertsMaxT, kMaxRoutes = kExpertsMaxK * kMaxTok;
 constexpr int kMaxList = kMaxRoutes + 2;  // entries: at most one a route, and the shared expert's two
 constexpr int kNoTok = 255;
 

@@ -158,7 +158,7 @@ size_t linear_fp8_workspace(int T, int K, int N);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s);  // tensor cores
 int64_t linear_fp8_tc_cost(int T, int K, int N);  // its time in 10 ns, without the launch
-constexpr int kExpertsMaxT = 16;
+constexpr int kExpertsMaxT = 16, kExpertsMaxE = 512, kExpertsMaxK = 16;  // tokens, experts, routes a token
 size_t experts_fp8_workspace(const fp4moe_dims& d);
 cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weights& w, const uint8_t* xq,
                                const float* xs, const int32_t* topk_idx, const float* topk_w, uint16_t* out, void* ws,
