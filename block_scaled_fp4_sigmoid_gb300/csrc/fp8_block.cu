@@ -205,7 +205,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 constexpr int32_t kMaxRows = 1 << 20;  // rows of one call
 constexpr int32_t kMaxCols = 65536;
 bool experts_sizes_ok(const fp4moe_dims& d) {
-  return d.T >= 1 && d.T <= kExpertsMaxT && d.H >= kBlk && d.H <= kMaxCols && d.H % kBlk == 0 && d.I >= kBlk &&
+  return d.T >= 0 && d.T <= kExpertsMaxT && d.H >= kBlk && d.H <= kMaxCols && d.H % kBlk == 0 && d.I >= kBlk &&
          d.I <= kMaxCols && d.I % kBlk == 0 && d.E >= 1 && d.E <= kExpertsMaxE && d.top_k >= 1 &&
          d.top_k <= kExpertsMaxK && (d.n_shared == 0 || d.n_shared == 1);
 }
@@ -290,6 +290,7 @@ fp4moe_status fp4moe_experts_fp8_block(const fp4moe_dims* dims, const fp4moe_fp8
                         (const void*)w->sh13_scale, (const void*)w->sh2_scale, (const void*)topk_idx,
                         (const void*)topk_w})
     if (!aligned(q, 4)) return FP4MOE_ERR_INVALID_ARG;
+  if (dims->T == 0) return FP4MOE_OK;
   if (fp4moe_status st = check_device()) return st;
   return cuda_status(
       launch_experts_fp8(*dims, *w, xq, xs, topk_idx, topk_w, out, ws, static_cast<cudaStream_t>(stream)));

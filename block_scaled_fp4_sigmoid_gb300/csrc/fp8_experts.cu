@@ -416,7 +416,7 @@ int64_t hq_bytes(const fp4moe_dims& d) { return list_cap(d) * 8 * d.I; }  // a m
 }  // namespace
 
 size_t experts_fp8_workspace(const fp4moe_dims& d) {
-  return (size_t)(hq_bytes(d) + list_cap(d) * 8 * (d.I / kBlk) * 4);
+  return (size_t)std::max<int64_t>(256, hq_bytes(d) + list_cap(d) * 8 * (d.I / kBlk) * 4);  // (0 says: unsupported)
 }
 
 cudaError_t launch_experts_fp8(const fp4moe_dims& d, const fp4moe_fp8_block_weights& w, const uint8_t* xq,

@@ -216,10 +216,11 @@ def experts_fp8_block(xq, xs, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, sh
         ws = torch.empty(n, dtype=torch.uint8, device=xq.device)
     else:
         _check_ws(ws, dev)
-    weights = Fp8BlockWeights(w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), _ptr(sh13),
-                              _ptr(sh13_scale), _ptr(sh2), _ptr(sh2_scale))
-    _experts(dims, weights, xq.data_ptr(), xs.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(),
-             ws.data_ptr(), ws.numel(), _stream(dev))
+    if T:
+        weights = Fp8BlockWeights(w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), _ptr(sh13),
+                                  _ptr(sh13_scale), _ptr(sh2), _ptr(sh2_scale))
+        _experts(dims, weights, xq.data_ptr(), xs.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(),
+                 ws.data_ptr(), ws.numel(), _stream(dev))
     return out
 
 

@@ -506,9 +506,10 @@ typedef struct {
  * that another rank holds) adds nothing; a token without any gives zeros; an
  * expert chosen twice by a token counts with the sum of its weights.  Only
  * chosen experts' weights are read, each once for all its tokens.
- * dims->fmt FP4MOE_FP8; 1 <= T <= 16, 128 <= H, I <= 65536, both multiples of
- * 128, 1 <= E <= 512, 1 <= top_k <= 16 (more than E where other ranks hold the
- * rest), n_shared 0 or 1; the routing parameters of dims are not used.
+ * dims->fmt FP4MOE_FP8; 0 <= T <= 16 (T = 0: nothing is done), 128 <= H, I <=
+ * 65536, both multiples of 128, 1 <= E <= 512, 1 <= top_k <= 16 (more than E
+ * where other ranks hold the rest), n_shared 0 or 1; the routing parameters
+ * of dims are not used.
  * ws: fp4moe_experts_fp8_block_workspace_size(dims) bytes (0: unsupported).
  * Codes, out and ws 16-byte aligned.  The result is the same on every run. */
 size_t fp4moe_experts_fp8_block_workspace_size(const fp4moe_dims *dims);

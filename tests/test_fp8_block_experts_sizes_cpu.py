@@ -54,3 +54,27 @@ def test_sizes_that_they_do_not_take(lib, kw):
     d = dims(**kw)
     assert lib.fp4moe_experts_fp8_block_workspace_size(ctypes.byref(d)) == 0
     assert call(lib, d, ws_bytes=1 << 40) == SHAPE
+
+
+def test_a_call_without_tokens_does_nothing(lib):
+    d = dims(T=0)
+    n = fm.experts_fp8_block_workspace_size(d)
+    assert n > 0
+    assert call(lib, d, ws_bytes=n) == 0
+    assert call(lib, d, xq=None) == INVALID
+
+
+def test_the_tensor_function_without_tokens():
+    """A batch that is empty on this rank: an empty output, nothing launched (there is no device here)."""
+    torch = pytest.importorskip("torch")
+    from block_scaled_fp4_sigmoid_gb300 import fp8_block as fb
+    E, H, I = 4, 256, 128
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(fb, "_device", lambda t: t.get_device())
+        m.setattr(fb, "_current_device", lambda: -1)
+        m.setattr(fb, "_experts", lambda *a: pytest.fail("launched"))
+        u8, f32 = lambda *s: torch.zeros(s, dtype=torch.uint8), lambda *s: torch.zeros(s)  # noqa: E731
+        out = torch.zeros((0, H), dtype=torch.bfloat16)
+        got = fb.experts_fp8_block(u8(0, H), f32(0, 2), torch.zeros((0, 2), dtype=torch.int32), f32(0, 2), u8(E, 2 * I, H),
+                                   f32(E, 2, 2), u8(E, H, I), f32(E, 2, 1), out=out)
+    assert got is out
