@@ -176,6 +176,8 @@ def linear_fp8_block(xq, xs, w, w_scale, *, out=None, out_dtype=torch.bfloat16, 
         _linear(T, K, N, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
                 out.stride(0) if T > 1 else N, out.dtype is _f32, None if ws is None else ws.data_ptr(),
                 0 if ws is None else ws.numel(), _stream(dev))
+    elif ws is not None:
+        ws.view(-1)[:64].zero_()  # the status word
     return out
 
 

@@ -461,7 +461,8 @@ fp4moe_status fp4moe_swiglu_fp8(const uint16_t *gu, int64_t gu_ld, int32_t T, in
 /* Block-scaled FP8 linear: out[t, n] = sum over K blocks b of
  *   xs[t, b] * w_scale[n / 128, b] * sum_{k in b} xq[t, k] * w[n, k].
  * out: bf16 (out_is_fp32 = 0) or fp32 [T, N] with row stride out_ld elements
- * (>= N).  0 <= T <= 2^20, 16 <= K <= 65536, K % 16 == 0, 1 <= N <= 2^20.
+ * (>= N).  0 <= T <= 2^20 (T = 0: nothing is done, and ws is left as it is),
+ * 16 <= K <= 65536, K % 16 == 0, 1 <= N <= 2^20.
  * xq and w 16-byte aligned.  ws: fp4moe_linear_fp8_block_workspace_size bytes
  * (0: unsupported sizes), the status word that each call clears and that
  * fp4moe_get_status reads (FP4MOE_ERR_TIMEOUT: a device-side wait ran out and

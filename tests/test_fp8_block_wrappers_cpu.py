@@ -163,3 +163,11 @@ def test_a_layer_object_keeps_nothing_that_its_calls_write(fb, launches, monkeyp
         assert not inside or any(t is w for w in weights)
     with pytest.raises(Exception, match="UNSUPPORTED|unsupported"):
         moe(fb, T=17)  # refused when the layer is made, as before
+
+
+def test_an_empty_product_leaves_a_clear_status(fb, launches):
+    """A call clears the status word of its workspace, one without tokens as well."""
+    ws = torch.full((256,), 0xA5, dtype=torch.uint8)
+    out = fb.linear_fp8_block(*linear_args(T=0), out=bf16(0, 128), ws=ws)
+    assert out.shape == (0, 128) and not launches.seen
+    assert not ws[:64].any() and bool((ws[64:] == 0xA5).all())
