@@ -131,10 +131,12 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, int rank, const uint32
 }
 
 // A scale load that stays where it is written (volatile): moved down to its
-// first use, its whole latency would show in every K block.
+// first use, its whole latency would show in every K block.  A plain load: the
+// read-only path asks for memory that nothing writes while this kernel runs, and
+// the launch before, which may write the scales, ends after this one has begun.
 __device__ __forceinline__ float fetch1(const float* p) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
 
