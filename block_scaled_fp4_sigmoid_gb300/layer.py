@@ -13,6 +13,7 @@ per expert and weight tensor).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -26,6 +27,19 @@ from . import (FP8, MXFP4, NVFP4, Debug, Fp8Weights, Weights, check_scales, emul
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
+
+
+def _on_device(method):
+    """The layer's device is made current for the call: the library launches on
+    the thread's current device, and the default stream's handle is the same
+    number on every device."""
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        if torch.cuda.current_device() == self.device.index:
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(self.device):
+            return method(self, *args, **kwargs)
+    return call
 
 
 def column_block(H: int, rank: int, world: int, unit: int = 128) -> tuple[int, int]:
@@ -101,6 +115,7 @@ class MoELayer:
                                _ptr(self.sh2_t), _ptr(self.sh2_scale), _ptr(self.w_router), _ptr(self.bias),
                                packed)
 
+    @_on_device
     def _check_scales(self):
         """Refuses weights with NaN block scales (fp4moe_check_scales): the
         layer does not test its scales on every call."""
@@ -113,6 +128,7 @@ class MoELayer:
         if st != 0:
             raise ValueError(f"{n} NaN block-scale bytes in the expert weights (status {st})")
 
+    @_on_device
     def _pack_w(self, codes, n_mat, rows, kbytes, gateup=False, slabs=False):
         dst = torch.empty(packed_weights_bytes(n_mat, rows, kbytes), dtype=torch.uint8, device=codes.device)
         s = torch.cuda.current_stream(codes.device).cuda_stream
@@ -124,6 +140,7 @@ class MoELayer:
             pack_weights(codes.data_ptr(), dst.data_ptr(), n_mat, rows, kbytes, s)
         return dst
 
+    @_on_device
     def _pack(self, raw, n_mat, rows, kblocks, gateup=False, slabs=False):
         dst = torch.empty(packed_scales_bytes(n_mat, rows, kblocks, self.fmt), dtype=torch.uint8,
                           device=raw.device)
@@ -143,6 +160,7 @@ class MoELayer:
         elems = 3 * d.H * d.I
         return elems // 2 + elems // blk
 
+    @_on_device
     def forward(self, x, out=None, debug: Debug | None = None, stream=None):
         d = self.dims
         if out is None:
@@ -151,6 +169,7 @@ class MoELayer:
         forward(d, self.weights, x.data_ptr(), out.data_ptr(), self.ws.data_ptr(), self.ws_bytes, s, debug)
         return out
 
+    @_on_device
     def forward_cols(self, x, h_begin: int, h_end: int, out=None, debug: Debug | None = None, stream=None):
         """The layer output restricted to columns [h_begin, h_end); the other
         columns of out are zero (fp4moe_forward_cols)."""
@@ -162,6 +181,7 @@ class MoELayer:
                      self.ws_bytes, s, debug)
         return out
 
+    @_on_device
     def forward_emulated(self, x, out=None, debug: Debug | None = None, stream=None):
         """NVFP4 layers only: the same layer in emulation mode
         (fp4moe_forward_nvfp4_emulated: BF16 dequantised experts, NVFP4 QDQ
@@ -189,6 +209,9 @@ class MoELayer:
     @classmethod
     def synthetic(cls, cfg, device="cuda", packed: bool | int = True):
         import synth
+        if torch.device(device).index not in (None, torch.cuda.current_device()):
+            with torch.cuda.device(device):
+                return cls.synthetic(cfg, device, packed)
         fmt = NVFP4 if cfg.fmt == "nvfp4" else MXFP4
         dims = make_dims(cfg.T, cfg.H, cfg.I, cfg.E, cfg.top_k, cfg.n_group, cfg.topk_group, cfg.n_shared,
                          cfg.routed_scaling, cfg.renormalize, fmt)
@@ -266,6 +289,7 @@ class MoELayer:
                             _ptr(v.w_router), _ptr(v.bias), v.packed)
         return v
 
+    @_on_device
     def synthetic_x(self, t0: int = 0, t1: int | None = None):
         """Activations of the synthetic configuration, drawn on the device."""
         import synth
@@ -290,6 +314,11 @@ class W8A8Layer:
         self.device = mx.device
         self.dims = make_dims(d.T, d.H, d.I, d.E, d.top_k, d.n_group, d.topk_group, d.n_shared, d.routed_scaling,
                               d.renormalize, FP8)
+        self._convert()
+
+    @_on_device
+    def _convert(self):
+        mx, d = self.mx, self.mx.dims
         s = torch.cuda.current_stream(self.device).cuda_stream
         ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
 
@@ -322,6 +351,7 @@ class W8A8Layer:
         d = self.dims
         return 3 * d.H * d.I + 4 * (2 * d.I + d.H)
 
+    @_on_device
     def forward(self, x, out=None, debug: Debug | None = None, stream=None):
         d = self.dims
         if out is None:
