@@ -128,6 +128,8 @@ def lib() -> ctypes.CDLL:
         L.fp4moe_swiglu_fp8.argtypes = [vp, i64, i32, i32, vp, vp, vp]
         L.fp4moe_linear_fp8_block_workspace_size.argtypes = [i32, i32, i32]
         L.fp4moe_linear_fp8_block_workspace_size.restype = sz
+        L.fp4moe_linear_fp8_block_form.argtypes = [i32, i32, i32]
+        L.fp4moe_linear_fp8_block_form.restype = ctypes.c_char_p
         L.fp4moe_linear_fp8_block.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i64, i32, vp, sz, vp]
         L.fp4moe_linear_fp8_block_status.argtypes = [vp, P(i32), P(i64)]
         L.fp4moe_experts_fp8_block_workspace_size.argtypes = [P(Dims)]
@@ -285,6 +287,11 @@ def linear_fp8_block_workspace_size(T: int, K: int, N: int) -> int:
     if n == 0:
         raise Fp4MoeError(2, "fp4moe_linear_fp8_block_workspace_size")
     return n
+
+
+def linear_fp8_block_form(T: int, K: int, N: int) -> str:
+    """Which kernels a call of these sizes runs (fp4moe_linear_fp8_block_form)."""
+    return lib().fp4moe_linear_fp8_block_form(T, K, N).decode()
 
 
 def linear_fp8_block(T: int, K: int, N: int, xq: int, xs: int, w: int, w_scale: int, out: int, out_ld: int,

@@ -244,6 +244,10 @@ size_t fp4moe_linear_fp8_block_workspace_size(int32_t T, int32_t K, int32_t N) {
   return linear_fp8_workspace(T, K, N);
 }
 
+const char* fp4moe_linear_fp8_block_form(int32_t T, int32_t K, int32_t N) {
+  return fp4moe_linear_fp8_block_workspace_size(T, K, N) == 0 ? "unsupported" : T == 0 ? "none" : linear_fp8_form(T, K, N);
+}
+
 fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uint8_t* xq, const float* xs,
                                       const uint8_t* w, const float* w_scale, void* out, int64_t out_ld,
                                       int32_t out_is_fp32, void* ws, size_t ws_bytes, void* stream) {

@@ -115,19 +115,26 @@ __global__ void __launch_bounds__(32 * kStreamWarps, MIN_CTAS) linear_stream_ker
 
 size_t linear_fp8_workspace(int, int, int) { return 256; }
 
-// Weights streamed into mma.sync or through shared memory into the tensor cores: the
-// former starts 1 to 2 us sooner, the latter has no rounds of CTAs each with
-// a latency of its own, and reads the weights once where the former reads them for
+// Weights streamed into mma.sync, or through shared memory into the tensor cores:
+// the former starts 1 to 2 us sooner, the latter has no rounds of CTAs each with a
+// latency of its own, and reads the weights once where the former reads them for
 // every 16 tokens.  Up to 128 tokens the smaller of two estimates decides, both
 // fitted to measurements (stream, tensor cores): 8 x 7168 x 36864 42.0, 42.4 us;
 // 8 x 1024 x 131072 36.7, 26.8; 16 x 7168 x 36864 74.7, 42.1; 16 x 7168 x 2112 6.3,
-// 7.8; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  In 10 ns:
-static int64_t stream_cost(const LinearFp8Args& a) {
-  const int64_t sms = 152, nb = blocks128(a.K), ctas = (a.N + 15) / 16 * (a.T > 8 ? (a.T + 15) / 16 : 1);
+// 7.8; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  The stream's, in 10 ns:
+static int64_t stream_cost(int T, int K, int N) {
+  const int64_t sms = 152, nb = blocks128(K), ctas = (N + 15) / 16 * (T > 8 ? (T + 15) / 16 : 1);
   const int64_t rounds = (ctas + 3 * sms - 1) / (3 * sms);  // of three CTAs an SM
-  if (a.T > 8) return ctas <= sms ? 160 + nb * 7 : rounds * (150 + nb * 19);
-  return std::max(ctas <= 2 * sms ? 150 + nb * 5 : (ctas <= 4 * sms ? 1 : rounds) * (140 + nb * 8), (int64_t)a.K * a.N / 60000);  // (6 TB/s)
+  if (T > 8) return ctas <= sms ? 160 + nb * 7 : rounds * (150 + nb * 19);
+  return std::max(ctas <= 2 * sms ? 150 + nb * 5 : (ctas <= 4 * sms ? 1 : rounds) * (140 + nb * 8), (int64_t)K * N / 60000);  // (6 TB/s)
 }
+
+// The instance of linear_stream_kernel for a call, or the tensor cores.
+struct StreamChoice {
+  int nt, min_ctas, run;  // nt = 0: the tensor cores
+  bool ahead;
+  const char* name;
+};
 
 // The more CTAs share an SM, the fewer registers and so the fewer loads in
 // flight a warp.  With row tiles for all of them, two blocks a run and three CTAs
@@ -136,23 +143,41 @@ static int64_t stream_cost(const LinearFp8Args& a) {
 // 11.9; 7168 x 36864, 2304 tiles: 49.6 against 44.1).  Where the tiles hardly
 // cover the SMs, four blocks a run (7168 x 2112, 132 tiles: 4.4 us against 5.2;
 // 16 tokens 6.9 against 10.1).
-cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
-  const int64_t rows = (a.N + 15) / 16, sms = 152;
-  const int64_t chunks = a.T > 8 ? (a.T + 15) / 16 : 1, ctas = rows * chunks;
-  if (a.T > 128) return launch_linear_fp8_tc(a, s);
-  const int64_t stream = stream_cost(a) - 250;  // (what the tensor cores start later)
-  if (stream > (int64_t)a.K * a.N / 56000 && stream > linear_fp8_tc_cost(a.T, a.K, a.N)) return launch_linear_fp8_tc(a, s);
-  const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
-                       a.out_fp32 ? 1 : 0, a.T > 8 || ctas > sms};
-  const dim3 grid((unsigned)rows, (unsigned)chunks), block(32 * kStreamWarps);
-  if (a.T > 8) {
-    if (ctas <= sms) return launch_pdl(linear_stream_kernel<2, 1, 4>, grid, block, 0, s, p);
-    return launch_pdl(linear_stream_kernel<2, 3, 2>, grid, block, 0, s, p);
+static StreamChoice stream_choice(int T, int K, int N) {
+  const int64_t rows = (N + 15) / 16, sms = 152;
+  const int64_t ctas = rows * (T > 8 ? (T + 15) / 16 : 1);
+  if (T > 128) return {0, 0, 0, false, ""};
+  const int64_t stream = stream_cost(T, K, N) - 250;  // (what the tensor cores start later)
+  if (stream > (int64_t)K * N / 56000 && stream > linear_fp8_tc_cost(T, K, N)) return {0, 0, 0, false, ""};
+  if (T > 8) {
+    if (ctas <= sms) return {2, 1, 4, true, "stream 2x1x4 ahead"};
+    return {2, 3, 2, true, "stream 2x3x2 ahead"};
   }
-  if (ctas <= 2 * sms) return launch_pdl(linear_stream_kernel<1, 2, 4>, grid, block, 0, s, p);
+  if (ctas <= sms) return {1, 2, 4, false, "stream 1x2x4"};
+  if (ctas <= 2 * sms) return {1, 2, 4, true, "stream 1x2x4 ahead"};
   const int64_t at3 = (ctas + 3 * sms - 1) / (3 * sms) * 3, at4 = (ctas + 4 * sms - 1) / (4 * sms) * 4;  // CTA slots
-  if (at3 <= at4) return launch_pdl(linear_stream_kernel<1, 3, 2>, grid, block, 0, s, p);
-  return launch_pdl(linear_stream_kernel<1, 4, 1>, grid, block, 0, s, p);
+  if (at3 <= at4) return {1, 3, 2, true, "stream 1x3x2 ahead"};
+  return {1, 4, 1, true, "stream 1x4x1 ahead"};
+}
+
+const char* linear_fp8_form(int T, int K, int N) {
+  const StreamChoice c = stream_choice(T, K, N);
+  return c.nt ? c.name : linear_fp8_tc_form(T, K, N);
+}
+
+cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
+  const StreamChoice c = stream_choice(a.T, a.K, a.N);
+  if (c.nt == 0) return launch_linear_fp8_tc(a, s);
+  const StreamParams p{a.xq, a.w, a.xs, a.ws, a.out, a.out_ld, static_cast<int32_t*>(a.scratch), a.T, a.K, a.N,
+                       a.out_fp32 ? 1 : 0, c.ahead};
+  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.T + 8 * c.nt - 1) / (8 * c.nt))), block(32 * kStreamWarps);
+  switch (100 * c.nt + 10 * c.min_ctas + c.run) {
+    case 214: return launch_pdl(linear_stream_kernel<2, 1, 4>, grid, block, 0, s, p);
+    case 232: return launch_pdl(linear_stream_kernel<2, 3, 2>, grid, block, 0, s, p);
+    case 124: return launch_pdl(linear_stream_kernel<1, 2, 4>, grid, block, 0, s, p);
+    case 132: return launch_pdl(linear_stream_kernel<1, 3, 2>, grid, block, 0, s, p);
+    default: return launch_pdl(linear_stream_kernel<1, 4, 1>, grid, block, 0, s, p);
+  }
 }
 
 }  // namespace fp4moe

@@ -657,6 +657,12 @@ cudaError_t linear_fp8_status_word(int32_t** word) {
 
 int64_t linear_fp8_tc_cost(int T, int K, int N) { return choose(T, K, N).cost; }
 
+const char* linear_fp8_tc_form(int T, int K, int N) {
+  const TcChoice c = choose(T, K, N);
+  if (c.split > 1) return c.split == 2 ? "tensor 128 split 2" : c.split == 4 ? "tensor 128 split 4" : "tensor 128 split 8";
+  return c.wide == 0 ? "tensor 128" : c.wide == N ? "tensor 256" : "tensor 256 + 128";
+}
+
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s) {
   const TcChoice c = choose(a.T, a.K, a.N);
   if (c.split > 1) return launch_tc<128, true>(a, c.split, false, s);

@@ -157,6 +157,8 @@ cudaError_t linear_fp8_status_word(int32_t** word);  // the current device's, of
 size_t linear_fp8_workspace(int T, int K, int N);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 cudaError_t launch_linear_fp8_tc(const LinearFp8Args& a, cudaStream_t s);  // tensor cores
+const char* linear_fp8_form(int T, int K, int N);     // the kernels of a call
+const char* linear_fp8_tc_form(int T, int K, int N);  // ... on the tensor cores
 int64_t linear_fp8_tc_cost(int T, int K, int N);  // its time in 10 ns, without the launch
 constexpr int kExpertsMaxT = 16, kExpertsMaxE = 512, kExpertsMaxK = 16;  // tokens, experts, routes a token
 size_t experts_fp8_workspace(const fp4moe_dims& d);

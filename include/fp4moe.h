@@ -475,6 +475,14 @@ fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uin
                                       const uint8_t *w, const float *w_scale, void *out, int64_t out_ld,
                                       int32_t out_is_fp32, void *ws, size_t ws_bytes, void *stream);
 
+/* Which kernels a call of these sizes runs, as a static text for profiles and
+ * tests: "stream AxBxC" (weights streamed into the warps' products: tokens / 8,
+ * CTAs an SM, K blocks a run), with "ahead" where the first weights are
+ * fetched before the launch before it ends; "tensor 256", "tensor 128",
+ * "tensor 256 + 128" (two launches) or "tensor 128 split S" (clusters of S
+ * CTAs a tile); "none" for T = 0, "unsupported" for sizes that are refused. */
+const char *fp4moe_linear_fp8_block_form(int32_t T, int32_t K, int32_t N);
+
 /* Synchronises `stream`, reads and clears what the fp4moe_linear_fp8_block
  * calls without a workspace have recorded on the current device: *st the first
  * condition (FP4MOE_OK if none), *count how many.  Either output may be NULL. */
