@@ -131,6 +131,7 @@ def lib() -> ctypes.CDLL:
         L.fp4moe_linear_fp8_block_form.argtypes = [i32, i32, i32]
         L.fp4moe_linear_fp8_block_form.restype = ctypes.c_char_p
         L.fp4moe_linear_fp8_block.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i64, i32, vp, sz, vp]
+        L.fp4moe_linear_fp8_block_debug.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i64, i32, P(Debug), vp, sz, vp]
         L.fp4moe_linear_fp8_block_status.argtypes = [vp, P(i32), P(i64)]
         L.fp4moe_experts_fp8_block_workspace_size.argtypes = [P(Dims)]
         L.fp4moe_experts_fp8_block_workspace_size.restype = sz
@@ -142,7 +143,7 @@ def lib() -> ctypes.CDLL:
                      "fp4moe_clear_status",
                      "fp4moe_get_status", "fp4moe_route_noalloc", "fp4moe_route_noalloc_status",
                      "fp4moe_check_scales", "fp4moe_add_rmsnorm_fp8", "fp4moe_swiglu_fp8", "fp4moe_linear_fp8_block",
-                     "fp4moe_linear_fp8_block_status",
+                     "fp4moe_linear_fp8_block_debug", "fp4moe_linear_fp8_block_status",
                      "fp4moe_experts_fp8_block"):
             getattr(L, name).restype = i32
         _LIB = L
@@ -298,6 +299,13 @@ def linear_fp8_block(T: int, K: int, N: int, xq: int, xs: int, w: int, w_scale: 
                      out_is_fp32: bool, ws: int | None, ws_bytes: int, stream: int = 0) -> None:
     _ok(lib().fp4moe_linear_fp8_block(T, K, N, xq, xs, w, w_scale, out, out_ld, int(out_is_fp32), ws, ws_bytes,
                                       stream), "fp4moe_linear_fp8_block")
+
+
+def linear_fp8_block_debug(T: int, K: int, N: int, xq: int, xs: int, w: int, w_scale: int, out: int, out_ld: int,
+                           out_is_fp32: bool, debug: Debug, ws: int | None, ws_bytes: int, stream: int = 0) -> None:
+    """linear_fp8_block with the wait limit and the withheld stage of debug."""
+    _ok(lib().fp4moe_linear_fp8_block_debug(T, K, N, xq, xs, w, w_scale, out, out_ld, int(out_is_fp32),
+                                            ctypes.byref(debug), ws, ws_bytes, stream), "fp4moe_linear_fp8_block_debug")
 
 
 def linear_fp8_block_status(stream: int = 0) -> tuple[int, int]:

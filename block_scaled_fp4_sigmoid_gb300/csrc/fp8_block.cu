@@ -251,6 +251,14 @@ const char* fp4moe_linear_fp8_block_form(int32_t T, int32_t K, int32_t N) {
 fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uint8_t* xq, const float* xs,
                                       const uint8_t* w, const float* w_scale, void* out, int64_t out_ld,
                                       int32_t out_is_fp32, void* ws, size_t ws_bytes, void* stream) {
+  return fp4moe_linear_fp8_block_debug(T, K, N, xq, xs, w, w_scale, out, out_ld, out_is_fp32, nullptr, ws, ws_bytes,
+                                       stream);
+}
+
+fp4moe_status fp4moe_linear_fp8_block_debug(int32_t T, int32_t K, int32_t N, const uint8_t* xq, const float* xs,
+                                            const uint8_t* w, const float* w_scale, void* out, int64_t out_ld,
+                                            int32_t out_is_fp32, const fp4moe_debug* dbg, void* ws, size_t ws_bytes,
+                                            void* stream) {
   if (!xq || !xs || !w || !w_scale || !out) return FP4MOE_ERR_INVALID_ARG;
   const size_t need = fp4moe_linear_fp8_block_workspace_size(T, K, N);
   if (need == 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
@@ -260,7 +268,9 @@ fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uin
     return FP4MOE_ERR_INVALID_ARG;
   if (T == 0) return FP4MOE_OK;
   if (fp4moe_status st = check_device()) return st;
-  const LinearFp8Args a{T, K, N, xq, xs, w, w_scale, out, out_ld, out_is_fp32 != 0, ws};
+  const LinearFp8Args a{T, K, N, xq, xs, w, w_scale, out, out_ld, out_is_fp32 != 0, ws,
+                        dbg && dbg->wait_limit_ns > 0 ? (uint64_t)dbg->wait_limit_ns : 0,
+                        dbg && dbg->withhold_first_stage != 0};
   return cuda_status(launch_linear_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 

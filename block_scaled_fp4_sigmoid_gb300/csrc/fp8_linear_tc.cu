@@ -27,9 +27,12 @@
 // of K.
 //
 // Warp roles: warp 0 TMA producer, warps 1 and 2 MMA issuers, warps 4-11 epilogue
-// (warp groups of their own, with the larger register share).  Every wait
-// is bounded; a timeout records FP4MOE_ERR_TIMEOUT in the status word, drains
-// copies and MMAs in flight, frees tensor memory and returns.
+// (warp groups of their own, with the larger register share).  Every wait on a
+// barrier in shared memory is bounded; a timeout records FP4MOE_ERR_TIMEOUT in the
+// status word, drains copies and MMAs in flight, frees tensor memory and returns.
+// The two cluster barriers of a shared tile have no limit of their own: a CTA
+// comes to both whether its roles finished or gave up, so their peers wait as
+// long as the bounded waits may.
 #include <cuda.h>
 
 #include <algorithm>
@@ -65,6 +68,8 @@ struct TcParams {
   int xbytes, wbytes;     // of the last tiles' boxes
   int out_fp32, vec;      // vec: 16-byte stores are aligned
   int second;             // the second launch of a call: joins the first one's end, not its start
+  int withhold;           // test knob: CTA 0 never fills its first stage
+  uint64_t wait_ns;       // limit of the pipeline's waits (drains keep kWaitLimitNs)
 };
 
 template <int BN, bool SPLIT>
@@ -366,14 +371,14 @@ __global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kerne
   };
   // bounded wait with a warp-uniform outcome
   auto wait_w = [&](uint32_t bar, uint32_t par) {
-    return __all_sync(0xffffffffu, mbar_wait_abortable(bar, par, kWaitLimitNs, abort_v)) != 0;
+    return __all_sync(0xffffffffu, mbar_wait_abortable(bar, par, p.wait_ns, abort_v)) != 0;
   };
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kCtlRegs));
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int stage = 0;
+      int stage = p.withhold && blockIdx.x == 0 ? 1 : 0, kb = kb0 + stage;
       uint32_t phase = 0, armed = 0, armed_par = 0;
       bool ok = true;
       for (int tile = first; ok && tile < tiles; tile += step) {
@@ -386,8 +391,8 @@ __global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kerne
         const bool x1 = mt + 1 == p.plan.mtiles, w1 = nt + 1 == p.plan.ntiles;
         const CUtensorMap *tmx = x1 ? &p.tmx1 : &p.tmx, *tmw = w1 ? &p.tmw1 : &p.tmw;
         const uint32_t bytes = (x1 ? p.xbytes : C::kABytes) + (w1 ? p.wbytes : C::kBBytes);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_abortable(smem_u32(&bar_empty[stage]), phase ^ 1u, kWaitLimitNs, abort_v)) {
+        for (; kb < kb1; ++kb) {
+          if (!mbar_wait_abortable(smem_u32(&bar_empty[stage]), phase ^ 1u, p.wait_ns, abort_v)) {
             ok = false;
             break;
           }
@@ -399,6 +404,7 @@ __global__ void __launch_bounds__(TcCfg<BN, SPLIT>::kThreads, 1) linear_tc_kerne
           tma_load_2d(base + C::kABytes, tmw, fb, kb * 128, nt * BN);
           if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
+        kb = kb0;
       }
       if (!ok) timed_out();
       for (int s = 0; s < C::kStages; ++s)  // every armed stage lands before the CTA exits
@@ -587,6 +593,8 @@ cudaError_t launch_tc(const LinearFp8Args& a, int split, bool second, cudaStream
   p.out_fp32 = a.out_fp32 ? 1 : 0;
   p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.out_ld * (a.out_fp32 ? 4 : 2) % 16 == 0;
   p.second = second ? 1 : 0;
+  p.withhold = a.withhold && !second;
+  p.wait_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -152,6 +152,8 @@ struct LinearFp8Args {
   int64_t out_ld;
   bool out_fp32;
   void* scratch;  // nullable: the status word of this call
+  uint64_t wait_ns;  // limit of the pipeline's waits; 0: kWaitLimitNs
+  bool withhold;     // test knob (fp4moe_debug.withhold_first_stage)
 };
 cudaError_t linear_fp8_status_word(int32_t** word);  // the current device's, of the calls without one
 size_t linear_fp8_workspace(int T, int K, int N);

@@ -475,6 +475,16 @@ fp4moe_status fp4moe_linear_fp8_block(int32_t T, int32_t K, int32_t N, const uin
                                       const uint8_t *w, const float *w_scale, void *out, int64_t out_ld,
                                       int32_t out_is_fp32, void *ws, size_t ws_bytes, void *stream);
 
+/* The same with the wait_limit_ns and withhold_first_stage of dbg (nullable; its
+ * other fields are not used): the pipeline waits of the tensor-core forms
+ * give up after wait_limit_ns, and with withhold_first_stage CTA 0 (of the
+ * first launch) never fills its first stage, so that they do.  The streamed
+ * forms wait for nothing and take no notice. */
+fp4moe_status fp4moe_linear_fp8_block_debug(int32_t T, int32_t K, int32_t N, const uint8_t *xq, const float *xs,
+                                            const uint8_t *w, const float *w_scale, void *out, int64_t out_ld,
+                                            int32_t out_is_fp32, const fp4moe_debug *dbg, void *ws, size_t ws_bytes,
+                                            void *stream);
+
 /* Which kernels a call of these sizes runs, as a static text for profiles and
  * tests: "stream AxBxC" (weights streamed into the warps' products: tokens / 8,
  * CTAs an SM, K blocks a run), with "ahead" where the first weights are
