@@ -1,9 +1,10 @@
 // Block-scaled FP8 activations: residual addition + RMS norm, and SwiGLU,
 // each with E4M3 codes and one fp32 scale per 128 columns.
 //
-// Both read their inputs once and write their outputs once (HBM bound): a
-// thread loads 8 consecutive columns at a time (16 bytes of bf16), 16 or 8 lanes
-// share a scale block, whose largest magnitude is a shuffle reduction.
+// Both read their inputs once and write their outputs once (HBM bound; the
+// norm up to 16384 columns): a thread loads 8 consecutive columns at a time (16
+// bytes of bf16), 16 or 8 lanes share a scale block, whose largest magnitude is a
+// shuffle reduction.
 #include <algorithm>
 
 #include "fp8_block.cuh"
@@ -65,7 +66,10 @@ __device__ __forceinline__ void quant_block(const float* v, bool in, uint8_t* q,
 // Up to two chunks the next row's inputs are fetched before this row's
 // reduction and stores, so that reads never pause: 4096 x 7168 with residual
 // and y in 42 us (6.3 TB/s) against 47 us with a CTA per row.  (With more
-// chunks they would not fit the registers.)
+// chunks they would not fit the registers.)  Longer rows are right but not
+// fast: from 16400 columns on the 64 registers of a thread of 1024 do not hold its
+// part of the row (2048 x 16384 52 us, 5.8 TB/s; 2048 x 16400 83 us, 3.6; 512 x
+// 65536 175 us, 1.7).
 template <int CH>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams p) {
   __shared__ float part[2][32];

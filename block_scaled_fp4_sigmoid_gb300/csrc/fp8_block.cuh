@@ -23,13 +23,13 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// Two fp32 values from the two bf16 halves of a word.
 // Starts `bytes` (a multiple of 16) at p, 16-byte aligned, on their way into L2.  No
 // hazard with a kernel that still writes them: L2 is where such writes arrive.
 __device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// Two fp32 values from the two bf16 halves of a word.
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

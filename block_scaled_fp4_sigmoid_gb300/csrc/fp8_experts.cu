@@ -263,8 +263,8 @@ int gateup_split(int64_t units, int hb) {
 // are in registers where column = token (T <= 8), else in its own shared memory
 // (GATHER).
 //
-// HBM bound, 6.6 TB/s over both kernels at 8 tokens and 384 experts (398 us for
-// 2.6 GB).  All loads of a run are issued together, 24 warps an SM: with one K
+// HBM bound, 6.3 to 6.6 TB/s over both kernels at 8 tokens and 384 experts (398 to
+// 417 us on several machines for 2.6 GB).  All loads of a run are issued together, 24 warps an SM: with one K
 // block a run the call took 428 us, with four (16 warps) 421, with one prefetched
 // a block ahead 435, with blocks copied ahead into shared memory by cp.async 485
 // and more.

@@ -121,7 +121,8 @@ size_t linear_fp8_workspace(int, int, int) { return 256; }
 // every 16 tokens.  Up to 128 tokens the smaller of two estimates decides, both
 // fitted to measurements (stream, tensor cores): 8 x 7168 x 36864 42.0, 42.4 us;
 // 8 x 1024 x 131072 36.7, 26.8; 16 x 7168 x 36864 74.7, 42.1; 16 x 7168 x 2112 6.3,
-// 7.8; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  The stream's, in 10 ns:
+// 7.8; 64 x 2048 x 512 2.7, 4.9; 32 x 7168 x 2112 12.5, 7.9.  This is the estimate of
+// the stream, in units of 10 ns.
 static int64_t stream_cost(int T, int K, int N) {
   const int64_t sms = 152, nb = blocks128(K), ctas = (N + 15) / 16 * (T > 8 ? (T + 15) / 16 : 1);
   const int64_t rounds = (ctas + 3 * sms - 1) / (3 * sms);  // of three CTAs an SM

@@ -248,7 +248,9 @@ class Fp8BlockMoE:
     """A mixture-of-experts feed-forward sublayer for up to 16 tokens: norm ->
     router (fp4moe_route on the bf16 norm output) -> experts (and the shared
     one) on block-scaled FP8 weights.  dims: as make_dims returns for the
-    layer with fmt=FP8; w_router bf16 [E, H], bias fp32 [E].  The object keeps
+    layer with fmt=FP8; w_router bf16 [E, H], bias fp32 [E].  It holds every
+    expert that its router chooses from: a rank with some of them calls
+    experts_fp8_block itself, with routes of -1 for the others'.  The object keeps
     its weights only: each call's scratch comes from the allocator, so calls on
     several streams do not meet."""
 

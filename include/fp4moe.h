@@ -524,7 +524,7 @@ typedef struct {
  * [T, top_k] as fp4moe_route writes them.  A route outside [0, E) (an expert
  * that another rank holds) adds nothing; a token without any gives zeros; an
  * expert chosen twice by a token counts with the sum of its weights.  Only
- * chosen experts' weights are read, each once for all its tokens.
+ * chosen experts' weights are read, each once for every eight of its tokens.
  * dims->fmt FP4MOE_FP8; 0 <= T <= 16 (T = 0: nothing is done), 128 <= H, I <=
  * 65536, both multiples of 128, 1 <= E <= 512, 1 <= top_k <= 16 (more than E
  * where other ranks hold the rest), n_shared 0 or 1; the routing parameters

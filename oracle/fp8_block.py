@@ -4,6 +4,10 @@ with one fp32 scale per row and 128 columns, or per 128 x 128 weight block.
     scale = fp32(amax / 448),  code = RNE_E4M3(fp32(v / scale)), saturating;
     a scale that is not positive gives signed zeros.
 
+(The kernels multiply by fp32(1 / scale), which can move a value by a few fp32
+units before its rounding: where v / scale lies that near a boundary between two
+codes, either is accepted.)
+
 Each function returns the exact result (in float64, from the values the codes
 and scales stand for) together with what bounds the error of an fp32
 evaluation of it, so that the tests can derive their tolerances.
