@@ -956,7 +956,14 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
       if (w.n > 0 && t < w.tiles && !(ok = wait_w(&bar_o[t][side(steps - 1)], kThree ? turn_of(steps - 1) : outs++))) break;
       ++queries;
       tc_fence_after();
-      if (t < w.tiles) {
+      if (t < w.tiles && w.n == 0) {
+        // Nothing in sight: zeros, a token a warp.  Not by way of shared memory: with E4M3 caches that is Q's, and the
+        // next piece's Q may be on its way.
+        const int cols = a.group * D;
+        for (int tk = t * p.tile_tokens + (warp & 3); tk < min((int)w.it.tokens, (t + 1) * p.tile_tokens); tk += 4)
+          for (int c = 0; c < cols; c += 128)
+            store_cols128(a.out, w.it.row0 + tk, w.it.kh * cols + c, cols - c, lane, make_float4(0, 0, 0, 0));
+      } else if (t < w.tiles) {
         // rows rr of the warp: where they go
         const bool parts = w.it.parts > 1;
         const float f = parts ? 1.f : l == 0.f ? 0.f : (FP8 ? a.kv.v_scale[w.it.kh] : 1.f) / l;

@@ -1,0 +1,78 @@
+"""More cases of the paged-attention operators: batches with rows that see nothing."""
+import numpy as np
+import pytest
+
+import block_scaled_fp4_sigmoid_gb300 as fm
+from gpu_util import ensure_built, torch_cuda
+from paged_util import Problem, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pa():
+    torch_cuda()
+    ensure_built()
+    from block_scaled_fp4_sigmoid_gb300 import paged_attention
+    return paged_attention
+
+
+def run(pa, p, t, **more):
+    return pa.prompt_attention(t["q"], t["k_cache"], t["v_cache"], t["starts"], t["lens"], t["table"], **p.options(t), **more)
+
+
+# ------------------------------------------------------------- pieces of work that see nothing
+ROWS, LENS = [600, 500, 1], [700, 500, 33]  # 10 + 8 + 1 pieces of 64 rows, for each of 8 heads: one for each of 152 CTAs
+WHOLE = {}
+
+
+def whole(pa, D, fp8):
+    """The sequences on their own, and what they give, checked."""
+    if (D, fp8) not in WHOLE:
+        p = Problem(LENS, rows=ROWS, hq=32, hkv=8, D=D, page=32, fp8=fp8, seed=60)
+        t = p.tensors()
+        out = run(pa, p, t)
+        check(out.double().cpu().numpy(), *p.expected())
+        WHOLE[D, fp8] = p, t, out, run(pa, p, t, fp8=True)
+    return WHOLE[D, fp8]
+
+
+def among_rows_that_see_nothing(pa, order, D, fp8):
+    """order: R, the sequences above, and E, as many pieces of work that see nothing (of one row: padding, rows
+    before position 0, rows past the table), as each CTA meets them, which is from the last row on."""
+    import torch
+    p, t, want, (codes, scales) = whole(pa, D, fp8)
+    reach = p.table.shape[1] * p.page
+    rows, lens, table, q, real = [], [], [], [], []
+    noise = torch.randn(19, 32, D, device="cuda").bfloat16()
+    for o in reversed(order):
+        if o == "R":
+            rows += ROWS
+            lens += LENS
+            table.append(t["table"])
+            q.append(t["q"])
+        else:
+            rows += [1] * 19
+            lens += [(0, -5, reach + 1 + i)[i % 3] for i in range(19)]
+            table.append(t["table"][[i % 3 for i in range(19)]])
+            q.append(noise)
+        real += [o == "R"] * len(q[-1])
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    u = {**t, "q": torch.cat(q), "table": torch.cat(table), "lens": ints(lens), "starts": ints(np.cumsum([0] + rows).tolist())}
+    real = torch.tensor(real, device="cuda")
+    n = order.count("R")
+    for _ in range(10):
+        got = run(pa, p, u)
+        assert torch.equal(got[real], want.repeat(n, 1, 1)) and not got[~real].any()
+        c, s = run(pa, p, u, fp8=True)
+        assert torch.equal(c[real], codes.repeat(n, 1)) and torch.equal(s[real], scales.repeat(n, 1))
+        assert not c[~real].any() and not s[~real].any()
+    assert fm.attn_prompt_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["EER", "EERR", "EEREER", "REE"])
+def test_prompt_rows_that_see_nothing_leave_the_next_queries(pa, order, D, fp8):
+    """Zeros of such rows do not go where the next rows' queries are, nor the other way."""
+    among_rows_that_see_nothing(pa, order, D, fp8)
