@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
       }
       if (!ok) break;
       if (w.n > 0 && t < w.tiles && !(ok = wait_w(&bar_o[t][side(steps - 1)], kThree ? turn_of(steps - 1) : outs++))) break;
-      ++queries;
+      if (w.n > 0) ++queries;  // (as the others count them: Q is loaded for pieces with something in sight)
       tc_fence_after();
       if (t < w.tiles && w.n == 0) {
         // Nothing in sight: zeros, a token a warp.  Not by way of shared memory: with E4M3 caches that is Q's, and the

@@ -76,3 +76,46 @@ def among_rows_that_see_nothing(pa, order, D, fp8):
 def test_prompt_rows_that_see_nothing_leave_the_next_queries(pa, order, D, fp8):
     """Zeros of such rows do not go where the next rows' queries are, nor the other way."""
     among_rows_that_see_nothing(pa, order, D, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["ER", "ERR", "RER", "EEER", "EREER", "RERER", "RE"])
+def test_prompt_rows_that_see_nothing_leave_the_roles_in_step(pa, order, D, fp8):
+    """An odd number of such pieces before others, between and behind them."""
+    among_rows_that_see_nothing(pa, order, D, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_with_one_padding_row(pa, D, fp8):
+    """2560 rows and one of padding: some CTAs meet a piece that sees nothing first, others do not."""
+    import torch
+    p = Problem([2560, 0], rows=[2560, 1], hq=32, hkv=8, D=D, page=64, fp8=fp8, seed=61)
+    t = p.tensors()
+    alone = {**t, "q": t["q"][:-1], "lens": t["lens"][:1], "starts": t["starts"][:2], "table": t["table"][:1]}
+    want = run(pa, p, alone)
+    for _ in range(5):
+        got = run(pa, p, t)
+        assert torch.equal(got[:-1], want) and not got[-1].any()
+    # among the first rows are those that a CTA takes after the padding: in 64 bits
+    p.starts, p.lens, p.table, p.q = np.array([0, 256]), np.array([256]), p.table[:1], p.q[:256]
+    check(got[:256].double().cpu().numpy(), *p.expected())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_with_rows_before_the_first_position(pa, D, fp8):
+    """Pieces wholly before position 0, partly, and ordinary ones, as 60 sequences bring them."""
+    import torch
+    rng = np.random.default_rng(62)
+    rows = rng.integers(1, 150, 60)
+    lens = np.where(rng.random(60) < 0.5, rng.integers(0, 60, 60), rows + rng.integers(0, 100, 60))
+    p = Problem(lens.tolist(), rows=rows.tolist(), hq=16, hkv=4, D=D, page=16, fp8=fp8, seed=62)
+    t = p.tensors()
+    want, bound = p.expected()
+    got = run(pa, p, t)
+    check(got.double().cpu().numpy(), want, bound)
+    for _ in range(10):
+        assert torch.equal(run(pa, p, t), got)
+    assert fm.attn_prompt_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
