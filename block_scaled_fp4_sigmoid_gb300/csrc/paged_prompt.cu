@@ -1069,6 +1069,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
         }
       }
       if constexpr (FP8) {
+        fence_async_smem();  // (staged rows were written where TMA writes the next Q)
         __syncwarp();
         if (w.n > 0 && lane == 0) mbar_arrive(smem_u32(&bar_q_free));
       }

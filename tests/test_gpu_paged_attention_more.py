@@ -4,7 +4,7 @@ import pytest
 
 import block_scaled_fp4_sigmoid_gb300 as fm
 from gpu_util import ensure_built, torch_cuda
-from paged_util import Problem, check
+from paged_util import Problem, check, check_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -118,4 +118,23 @@ def test_prompt_with_rows_before_the_first_position(pa, D, fp8):
     check(got.double().cpu().numpy(), want, bound)
     for _ in range(10):
         assert torch.equal(run(pa, p, t), got)
+    assert fm.attn_prompt_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(32, 8, 64), (32, 8, 128), (48, 16, 128)])
+def test_prompt_outputs_staged_before_the_next_queries(pa, hq, hkv, D):
+    """E4M3 caches, five and more short pieces a CTA: each one's outputs leave by the memory that the next one's queries
+    arrive in.  bf16 and codes, the same every time."""
+    import torch
+    rows = [62 - i % 3 for i in range(100)]
+    p = Problem([n + 5 * i % 40 for i, n in enumerate(rows)], rows=rows, hq=hq, hkv=hkv, D=D, page=16, fp8=True, seed=63)
+    t = p.tensors()
+    want, bound = p.expected()
+    got, (codes, scales) = run(pa, p, t), run(pa, p, t, fp8=True)
+    check(got.double().cpu().numpy(), want, bound)
+    check_codes(codes.cpu().numpy(), scales.cpu().numpy(), want, bound)
+    for _ in range(100):
+        assert torch.equal(run(pa, p, t), got)
+        c, s = run(pa, p, t, fp8=True)
+        assert torch.equal(c, codes) and torch.equal(s, scales)
     assert fm.attn_prompt_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
