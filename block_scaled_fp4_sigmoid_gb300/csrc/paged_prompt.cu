@@ -392,6 +392,19 @@ __device__ __forceinline__ void fetch_out(uint32_t taddr, float l, float f, floa
   for (int x = 0; x < N; ++x) o[x] = l == 0.f ? 0.f : o[x] * f;
 }
 
+// `width` finished columns of one row from `col` on as zeros, by a warp.  (store_cols128 here had heads of 64 in E4M3 spill.)
+__device__ __forceinline__ void zero_cols(const PagedOut& o, int64_t row, int col, int width, int lane) {
+  const int64_t at = row * o.cols + col;
+  for (int c = 8 * lane; c < width; c += 256) {
+    if (o.out)
+      *reinterpret_cast<uint4*>(o.out + at + c) = make_uint4(0, 0, 0, 0);
+    else
+      *reinterpret_cast<uint2*>(o.codes + at + c) = make_uint2(0, 0);
+  }
+  if (!o.out)
+    for (int c = lane; c < width >> 7; c += 32) o.scales[row * (o.cols >> 7) + (col >> 7) + c] = 0.f;
+}
+
 // Pieces of a sequence whose rows are s0 .. s1 - 1.
 __device__ __forceinline__ int pieces_of(const PagedBatch& bt, int b, int per, int& s0, int& end) {
   s0 = max(0, bt.starts[b]);
@@ -781,7 +794,15 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
     uint32_t queries = 0, steps = 0, outs = 0;
     for (int k = 0; ok && k < count; ++k) {
       const Work w = work_of(items[k], a, p.tile_tokens);
-      if (w.it.tokens == 0) continue;
+      if (w.n == 0) {
+        // Nothing in sight: zeros, a token a warp.  Not by way of shared memory: with E4M3 caches that is Q's, and the
+        // next piece's Q may be on its way.  (Q is not loaded for such a piece, and no role counts it.)
+        const int cols = a.group * D;
+        for (int tk = t * p.tile_tokens + (warp & 3); tk < min((int)w.it.tokens, (t + 1) * p.tile_tokens); tk += 4)
+          zero_cols(a.out, w.it.row0 + tk, w.it.kh * cols, cols, lane);
+        __syncwarp();
+        continue;
+      }
       if (w.n > 4096) *long_v = 1;
       const int tok = t * p.tile_tokens + row_tok;
       const bool mine = row_in && tok < w.it.tokens;
@@ -792,48 +813,46 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
                 all_sinks = __reduce_min_sync(0xffffffffu, mine ? seen.sinks : 1 << 30);
       float scale = a.scale_log2;
       bool spoilt = false;
-      if (w.n > 0) {
-        if constexpr (FP8) {
-          // Q as the sum of two E4M3 numbers, for products with the cache's codes as they are.
-          // Scaled by the power of two that brings a row's largest magnitude to 128 .. 256, the 8 bits
-          // of a bf16 value are the first number's 4 and a remainder of 4: exact down to 2^-10 of
-          // the largest, and off by 2^-18 of it at most below.
-          if (!(ok = wait_w(&bar_q, queries & 1))) break;
-          if (t < w.tiles) {
-            uint4 q[D / 8];
-            float amax = 0.f;
+      if constexpr (FP8) {
+        // Q as the sum of two E4M3 numbers, for products with the cache's codes as they are.
+        // Scaled by the power of two that brings a row's largest magnitude to 128 .. 256, the 8 bits
+        // of a bf16 value are the first number's 4 and a remainder of 4: exact down to 2^-10 of
+        // the largest, and off by 2^-18 of it at most below.
+        if (!(ok = wait_w(&bar_q, queries & 1))) break;
+        if (t < w.tiles) {
+          uint4 q[D / 8];
+          float amax = 0.f;
 #pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-              q[x] = lds128(sq + t * C::kTile + (x >> 3) * kPanel + r * 128 + (((x & 7) ^ (r & 7)) << 4));
+          for (int x = 0; x < D / 8; ++x) {
+            q[x] = lds128(sq + t * C::kTile + (x >> 3) * kPanel + r * 128 + (((x & 7) ^ (r & 7)) << 4));
 #pragma unroll
-              for (uint32_t y : {q[x].x, q[x].y, q[x].z, q[x].w}) amax = max_nan(amax, max_nan(fabsf(bf16_lo(y)), fabsf(bf16_hi(y))));
-            }
-            const int e = (int)(__float_as_uint(amax) >> 23 & 255u);
-            const int x2 = e == 0 || e == 255 ? 0 : min(max(e - 134, -100), 100);
-            const float down = __uint_as_float((uint32_t)(127 - x2) << 23);
-            scale *= __uint_as_float((uint32_t)(127 + x2) << 23) * a.kv.k_scale[w.it.kh];
-            spoilt = e == 255;  // (codes saturate)
-            const uint32_t to_q = sq8 + t * C::kTile + r * D, swz = D == 128 ? r & 7 : (r >> 1) & 3;
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint4& v = q[2 * x + (y >> 1)];
-                const uint32_t u0 = y & 1 ? v.z : v.x, u1 = y & 1 ? v.w : v.y;
-                const float v0 = bf16_lo(u0) * down, v1 = bf16_hi(u0) * down, v2 = bf16_lo(u1) * down, v3 = bf16_hi(u1) * down;
-                hi[y] = e4m3x4(v0, v1, v2, v3);
-                const float4 f = e4m3x4_values(hi[y]);
-                lo[y] = e4m3x4(v0 - f.x, v1 - f.y, v2 - f.z, v3 - f.w);
-              }
-              sts128(to_q + ((x ^ swz) << 4), hi[0], hi[1], hi[2], hi[3]);
-              sts128(to_q + kKeys * D + ((x ^ swz) << 4), lo[0], lo[1], lo[2], lo[3]);
-            }
+            for (uint32_t y : {q[x].x, q[x].y, q[x].z, q[x].w}) amax = max_nan(amax, max_nan(fabsf(bf16_lo(y)), fabsf(bf16_hi(y))));
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bar_q16));
+          const int e = (int)(__float_as_uint(amax) >> 23 & 255u);
+          const int x2 = e == 0 || e == 255 ? 0 : min(max(e - 134, -100), 100);
+          const float down = __uint_as_float((uint32_t)(127 - x2) << 23);
+          scale *= __uint_as_float((uint32_t)(127 + x2) << 23) * a.kv.k_scale[w.it.kh];
+          spoilt = e == 255;  // (codes saturate)
+          const uint32_t to_q = sq8 + t * C::kTile + r * D, swz = D == 128 ? r & 7 : (r >> 1) & 3;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint4& v = q[2 * x + (y >> 1)];
+              const uint32_t u0 = y & 1 ? v.z : v.x, u1 = y & 1 ? v.w : v.y;
+              const float v0 = bf16_lo(u0) * down, v1 = bf16_hi(u0) * down, v2 = bf16_lo(u1) * down, v3 = bf16_hi(u1) * down;
+              hi[y] = e4m3x4(v0, v1, v2, v3);
+              const float4 f = e4m3x4_values(hi[y]);
+              lo[y] = e4m3x4(v0 - f.x, v1 - f.y, v2 - f.z, v3 - f.w);
+            }
+            sts128(to_q + ((x ^ swz) << 4), hi[0], hi[1], hi[2], hi[3]);
+            sts128(to_q + kKeys * D + ((x ^ swz) << 4), lo[0], lo[1], lo[2], lo[3]);
+          }
         }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_q16));
       }
       scale = fmaxf(scale, 1.17549435e-38f);  // (a scale of 0: masked scores stay -inf)
       if (spoilt) scale = __uint_as_float(0x7FC00000u);
@@ -953,17 +972,10 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
         ready(2);
       }
       if (!ok) break;
-      if (w.n > 0 && t < w.tiles && !(ok = wait_w(&bar_o[t][side(steps - 1)], kThree ? turn_of(steps - 1) : outs++))) break;
-      if (w.n > 0) ++queries;  // (as the others count them: Q is loaded for pieces with something in sight)
+      if (t < w.tiles && !(ok = wait_w(&bar_o[t][side(steps - 1)], kThree ? turn_of(steps - 1) : outs++))) break;
+      ++queries;
       tc_fence_after();
-      if (t < w.tiles && w.n == 0) {
-        // Nothing in sight: zeros, a token a warp.  Not by way of shared memory: with E4M3 caches that is Q's, and the
-        // next piece's Q may be on its way.
-        const int cols = a.group * D;
-        for (int tk = t * p.tile_tokens + (warp & 3); tk < min((int)w.it.tokens, (t + 1) * p.tile_tokens); tk += 4)
-          for (int c = 0; c < cols; c += 128)
-            store_cols128(a.out, w.it.row0 + tk, w.it.kh * cols + c, cols - c, lane, make_float4(0, 0, 0, 0));
-      } else if (t < w.tiles) {
+      if (t < w.tiles) {
         // rows rr of the warp: where they go
         const bool parts = w.it.parts > 1;
         const float f = parts ? 1.f : l == 0.f ? 0.f : (FP8 ? a.kv.v_scale[w.it.kh] : 1.f) / l;
@@ -1071,7 +1083,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
       if constexpr (FP8) {
         fence_async_smem();  // (staged rows were written where TMA writes the next Q)
         __syncwarp();
-        if (w.n > 0 && lane == 0) mbar_arrive(smem_u32(&bar_q_free));
+        if (lane == 0) mbar_arrive(smem_u32(&bar_q_free));
       }
     }
     if (!ok && lane == 0) timed_out();
