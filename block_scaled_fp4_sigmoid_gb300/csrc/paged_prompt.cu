@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
           const int x2 = e == 0 || e == 255 ? 0 : min(max(e - 134, -100), 100);
           const float down = __uint_as_float((uint32_t)(127 - x2) << 23);
           scale *= __uint_as_float((uint32_t)(127 + x2) << 23) * a.kv.k_scale[w.it.kh];
-          spoilt = e == 255;  // (codes saturate)
+          spoilt = e == 255;  // (infinities saturate: such a row is computed key by key if it sees anything)
           const uint32_t to_q = sq8 + t * C::kTile + r * D, swz = D == 128 ? r & 7 : (r >> 1) & 3;
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
@@ -855,7 +855,6 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
         if (lane == 0) mbar_arrive(smem_u32(&bar_q16));
       }
       scale = fmaxf(scale, 1.17549435e-38f);  // (a scale of 0: masked scores stay -inf)
-      if (spoilt) scale = __uint_as_float(0x7FC00000u);
       const float grow = fminf(8.f / scale, 3.0e38f);  // (finite: a first maximum is always taken)
       float m = -INFINITY, l = 0.f;
       for (int i = 0; t < w.tiles && i < w.n; ++i, ++steps) {
@@ -995,7 +994,8 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
           for (int x = 0; x < 32; ++x) most[x & 3] = max_nan(most[x & 3], fabsf(o[x]));
         }
         float amax = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3]));
-        const bool by_key = __any_sync(0xffffffffu, mine && l == l && !(amax <= 3.4028235e38f));
+        const bool by_key =
+            __any_sync(0xffffffffu, mine && ((l == l && !(amax <= 3.4028235e38f)) || (spoilt && m != -INFINITY)));
         if (by_key) *long_v = 1;
         if (!by_key) {
           // through shared memory, so that stores cover whole rows (a row a lane: 4000 cycles)

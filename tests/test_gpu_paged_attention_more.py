@@ -1,10 +1,12 @@
-"""More cases of the paged-attention operators: batches with rows that see nothing."""
+"""More cases of the paged-attention operators: batches with rows that see nothing, and queries
+at the ends of their range."""
 import numpy as np
 import pytest
 
 import block_scaled_fp4_sigmoid_gb300 as fm
 from gpu_util import ensure_built, torch_cuda
 from paged_util import Problem, check, check_codes
+from oracle.formats import E4M3_TABLE
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +140,40 @@ def test_prompt_outputs_staged_before_the_next_queries(pa, hq, hkv, D):
         c, s = run(pa, p, t, fp8=True)
         assert torch.equal(c, codes) and torch.equal(s, scales)
     assert fm.attn_prompt_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
+
+
+# ------------------------------------------------------------- queries at the ends of their range, and beyond
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_prompt_queries_that_are_not_finite_and_see_nothing(pa, D, value):
+    """E4M3 caches: rows before position 0 and rows over holes only, in a tile with others that see something, are
+    zeros whatever their queries hold."""
+    p = Problem([40, 60], rows=[60, 60], hq=8, hkv=2, D=D, page=16, fp8=True, seed=50)
+    p.table[1, 0] = -1  # positions 0 .. 15 of the second sequence
+    blind = np.r_[0:20, 60:76]
+    p.q[blind, :, 3] = value
+    t = p.tensors()
+    p.q[blind] = 0
+    want, bound = p.expected()
+    assert (want[blind] == 0).all()
+    check(run(pa, p, t).double().cpu().numpy(), want, bound)
+    codes, scales = run(pa, p, t, fp8=True)
+    check_codes(codes.cpu().numpy(), scales.cpu().numpy(), want, bound)
+    assert not (codes.cpu().numpy()[blind] & 0x7F).any()
+
+
+@pytest.mark.parametrize("D,n", [(64, 60), (128, 60), (128, 5000)])
+def test_prompt_infinite_queries(pa, D, n):
+    """E4M3 caches (5000: in parts): q holds one infinity, against keys whose value there is of one
+    sign.  Scores are all -infinity: zeros; all +infinity: NaN.  The other rows are what they are."""
+    p = Problem([n, n], rows=[30, 30], hq=8, hkv=2, D=D, page=16, fp8=True, seed=51)
+    p.kc[..., 3] = np.where((p.kc[..., 3] & 0x7F) == 0x7F, p.kc[..., 3], 0x28)
+    p.k = E4M3_TABLE[p.kc] * p.ks.astype(np.float64)[:, None, None]
+    p.q[[4, 40], :, 3], p.q[[5, 41], :, 3] = -np.inf, np.inf
+    t = p.tensors()
+    got = run(pa, p, t).double().cpu().numpy()
+    finite = np.delete(np.arange(60), [4, 5, 40, 41])
+    p.q[[4, 5, 40, 41]] = 0
+    want, bound = p.expected()
+    check(got[finite], want[finite], bound[finite])
+    assert (got[[4, 40]] == 0).all() and np.isnan(got[[5, 41]]).all()
