@@ -271,8 +271,8 @@ __device__ __forceinline__ void attend(const PagedAttn& a, const Groups& gr, int
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int e = (int)(__float_as_uint(amax) >> 23);
-      const int k = e == 0 || e == 255 ? 0 : min(max(e - 127, -100), 100);
+      // (infinities stay, and nothing beside them becomes one; both powers are normal numbers)
+      const int k = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
       const float down = __uint_as_float((uint32_t)(127 - k) << 23), up = __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
       for (int i = 0; i < 2; ++i) qs[n][i] *= __shfl_sync(0xffffffffu, up, 4 * (2 * t + i)) * a.kv.k_scale[kh];

@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
             for (uint32_t y : {q[x].x, q[x].y, q[x].z, q[x].w}) amax = max_nan(amax, max_nan(fabsf(bf16_lo(y)), fabsf(bf16_hi(y))));
           }
           const int e = (int)(__float_as_uint(amax) >> 23 & 255u);
-          const int x2 = e == 0 || e == 255 ? 0 : min(max(e - 134, -100), 100);
+          const int x2 = max(e - 134, -126);  // (both powers are normal numbers)
           const float down = __uint_as_float((uint32_t)(127 - x2) << 23);
           scale *= __uint_as_float((uint32_t)(127 + x2) << 23) * a.kv.k_scale[w.it.kh];
           spoilt = e == 255;  // (infinities saturate: such a row is computed key by key if it sees anything)

@@ -19,8 +19,18 @@ def pa():
     return paged_attention
 
 
-def run(pa, p, t, **more):
+def run(pa, p, t, decode=False, **more):
+    if decode:
+        return pa.decode_attention(t["q"], t["k_cache"], t["v_cache"], t["lens"], t["table"], **p.options(t), **more)
     return pa.prompt_attention(t["q"], t["k_cache"], t["v_cache"], t["starts"], t["lens"], t["table"], **p.options(t), **more)
+
+
+def holds(pa, p, decode=False):
+    want, bound = p.expected()
+    t = p.tensors()
+    check(run(pa, p, t, decode).double().cpu().numpy(), want, bound)
+    codes, scales = run(pa, p, t, decode, fp8=True)
+    check_codes(codes.cpu().numpy(), scales.cpu().numpy(), want, bound)
 
 
 # ------------------------------------------------------------- pieces of work that see nothing
@@ -177,3 +187,26 @@ def test_prompt_infinite_queries(pa, D, n):
     want, bound = p.expected()
     check(got[finite], want[finite], bound[finite])
     assert (got[[4, 40]] == 0).all() and np.isnan(got[[5, 41]]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("power", [118, 104, -104, -118])
+def test_queries_near_the_ends_of_the_range(pa, power, decode, D, fp8):
+    """Queries of 2^power against keys of 2^-power: ordinary scores."""
+    rows = [1, 1, 1] if decode else [60, 17, 1]
+    p = Problem([600, 17, 130], rows=rows, hq=8, hkv=2, D=D, page=16, fp8=fp8, k_size=2.0 ** -power, seed=52)
+    p.q *= 2.0 ** power
+    holds(pa, p, decode)
+
+
+@pytest.mark.parametrize("D,n", [(64, 60), (128, 60), (128, 40000)])
+def test_decode_infinite_queries(pa, D, n):
+    """As above for decode, beside a large value, which is nothing next to an infinity."""
+    p = Problem([n, n], hq=8, hkv=2, D=D, page=16, fp8=True, seed=54)
+    p.kc[..., 3] = np.where((p.kc[..., 3] & 0x7F) == 0x7F, p.kc[..., 3], 0x28)
+    p.q[0, :, 3], p.q[1, :, 3] = -np.inf, np.inf
+    p.q[:, :, 4] = -3e38
+    got = run(pa, p, p.tensors(), True).double().cpu().numpy()
+    assert (got[0] == 0).all() and np.isnan(got[1]).all()
