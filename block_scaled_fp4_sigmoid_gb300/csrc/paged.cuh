@@ -85,6 +85,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// Softmax weights as fp16 operands for V out of an E4M3 cache.  fp16 has 11 bits where bf16 has 8, but its smallest
+// step is 2^-24: many small weights matter together, so they come here scaled by a power of two that brings the largest to 2^15
+// (the sums are in the same scale, which the division takes out).  At scores past 2^24 the scale's exponent is rounded:
+// the largest weight saturates then.
+__device__ __forceinline__ uint32_t f16x2_weights(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Four fp32 values of four E4M3 codes.
 __device__ __forceinline__ float4 e4m3x4_values(uint32_t w) {
   uint32_t lo, hi;

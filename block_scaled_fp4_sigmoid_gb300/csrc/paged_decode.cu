@@ -224,10 +224,10 @@ struct Joined {
     sum = sum * f + ml.y * e;
     top = now;
   }
-  // the output, v_scale included
+  // the output, v_scale included (not v_scale / sum, which may leave the range that the output is in)
   __device__ __forceinline__ float4 out(float v_scale) const {
-    const float f = sum == 0.f ? 0.f : v_scale / sum;
-    return make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    return make_float4(v.x * f * v_scale, v.y * f * v_scale, v.z * f * v_scale, v.w * f * v_scale);
   }
 };
 
@@ -293,6 +293,7 @@ __device__ __forceinline__ void attend(const PagedAttn& a, const Groups& gr, int
     m[n][0] = m[n][1] = -INFINITY;
     l[n][0] = l[n][1] = 0.f;
   }
+  constexpr float kUp = FP8 ? 15.f : 0.f;  // weights are scaled by 2^kUp (f16x2_weights)
   int stage = 0, ahead = C::kStages - 1;
   for (int i = i0 + warp * C::kGroups; i < i1; i += W * C::kGroups) {
     st.fetch(ahead);
@@ -389,13 +390,13 @@ __device__ __forceinline__ void attend(const PagedAttn& a, const Groups& gr, int
       uint32_t pf[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0], b1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+        const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kUp, b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kUp;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float e0 = exp2_approx(s[x][n][2 * h] - b0), e1 = exp2_approx(s[x][n][2 * h + 1] - b1);
           l[n][0] += e0;
           l[n][1] += e1;
-          pf[n][h] = movm_t(FP8 ? f16x2_rn(e0, e1) : bf16x2_rn(e0, e1));
+          pf[n][h] = movm_t(FP8 ? f16x2_weights(e0, e1) : bf16x2_rn(e0, e1));
         }
       }
       const uint32_t vt = base_at + x * 2 * C::kTile + C::kTile;

@@ -210,11 +210,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Operand formats of kind::f16: 0 fp16, 1 bf16; B of P V has its columns consecutive.
 template <bool FP8>
@@ -380,16 +375,16 @@ struct Rows {
   }
 };
 
-// N columns of this thread's row of O, times f; zeros where nothing is seen (then
-// what tensor memory holds means nothing).
+// N columns of this thread's row of O, times f and then vs (their product may leave the range that the output is in);
+// zeros where nothing is seen (then what tensor memory holds means nothing).
 template <int N = 32>
-__device__ __forceinline__ void fetch_out(uint32_t taddr, float l, float f, float* o) {
+__device__ __forceinline__ void fetch_out(uint32_t taddr, float l, float f, float vs, float* o) {
 #pragma unroll
   for (int x = 0; x < N; x += 32) tc_ld32(taddr + x, o + x);
   tc_wait_ld();
   landed<N>(o);
 #pragma unroll
-  for (int x = 0; x < N; ++x) o[x] = l == 0.f ? 0.f : o[x] * f;
+  for (int x = 0; x < N; ++x) o[x] = l == 0.f ? 0.f : o[x] * f * vs;
 }
 
 // `width` finished columns of one row from `col` on as zeros, by a warp.  (store_cols128 here had heads of 64 in E4M3 spill.)
@@ -856,6 +851,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
       }
       scale = fmaxf(scale, 1.17549435e-38f);  // (a scale of 0: masked scores stay -inf)
       const float grow = fminf(8.f / scale, 3.0e38f);  // (finite: a first maximum is always taken)
+      constexpr float kUp = FP8 ? 7.f : 0.f;  // weights, which may grow to 2^8, are scaled by 2^kUp (f16x2_weights)
       float m = -INFINITY, l = 0.f;
       for (int i = 0; t < w.tiles && i < w.n; ++i, ++steps) {
         const int j0 = w.at(w.i0 + i);
@@ -934,7 +930,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : -m * scale;
+        const float base = m == -INFINITY ? 0.f : kUp - m * scale;
         const uint64_t sc2 = pack2(scale, scale), ba2 = pack2(base, base);
         uint64_t sum[2] = {0, 0};
         uint32_t pk[32];
@@ -945,7 +941,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
             unpack2(fma2(pack2(s[2 * c], s[2 * c + 1]), sc2, ba2), x, y);
             x = exp2_approx(x), y = exp2_approx(y);
             sum[c & 1] = add2(sum[c & 1], pack2(x, y));
-            pk[c & 31] = FP8 ? f16x2_rn(x, y) : bf16x2_rn(x, y);
+            pk[c & 31] = FP8 ? f16x2_weights(x, y) : bf16x2_rn(x, y);
           }
         };
         auto ready = [&](int half) {
@@ -977,7 +973,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
       if (t < w.tiles) {
         // rows rr of the warp: where they go
         const bool parts = w.it.parts > 1;
-        const float f = parts ? 1.f : l == 0.f ? 0.f : (FP8 ? a.kv.v_scale[w.it.kh] : 1.f) / l;
+        const float f = parts ? 1.f : l == 0.f ? 0.f : 1.f / l, vs = FP8 && !parts ? a.kv.v_scale[w.it.kh] : 1.f;
         // (opaque, so that what depends on the lane alone is not kept in registers over all items)
         int ln = lane;
         asm volatile("" : "+r"(ln));
@@ -989,7 +985,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
-          fetch_out(to + 32 * c, l, f, o);
+          fetch_out(to + 32 * c, l, f, vs, o);
 #pragma unroll
           for (int x = 0; x < 32; ++x) most[x & 3] = max_nan(most[x & 3], fabsf(o[x]));
         }
@@ -1003,20 +999,20 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
-              fetch_out(to + 32 * c, l, f, o);
+              fetch_out(to + 32 * c, l, f, vs, o);
 #pragma unroll
               for (int x = 0; x < 8; ++x)
                 sts128(stg + staged<128>(ln, x), __float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
                        __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3]));
               to_rows.store<128, true>(reinterpret_cast<uint8_t*>(p.part + part_row * D + 32 * c), 4 * D, 0);
             }
-            if (mine) p.ml[part_row + r] = make_float2(m == -INFINITY ? m : m * scale, l);
+            if (mine) p.ml[part_row + r] = make_float2(m == -INFINITY ? m : m * scale - kUp, l);
           } else if (a.out.out) {
             uint8_t* dst = reinterpret_cast<uint8_t*>(a.out.out + (int64_t)w.it.row0 * a.out.cols + (int64_t)w.it.kh * a.group * D);
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
               float o[64];
-              fetch_out<64>(to + 64 * c, l, f, o);
+              fetch_out<64>(to + 64 * c, l, f, vs, o);
 #pragma unroll
               for (int x = 0; x < 8; ++x)
                 sts128(stg + staged<128>(ln, x), bf16x2_rn(o[8 * x], o[8 * x + 1]), bf16x2_rn(o[8 * x + 2], o[8 * x + 3]),
@@ -1030,7 +1026,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
-              fetch_out(to + 32 * c, l, f, o);
+              fetch_out(to + 32 * c, l, f, vs, o);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 uint32_t q[4];
@@ -1180,9 +1176,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
       top = now;
     }
   }
-  const float f = sum == 0.f ? 0.f : (FP8 ? a.kv.v_scale[it.kh] : 1.f) / sum;
+  const float f = sum == 0.f ? 0.f : 1.f / sum, vs = FP8 ? a.kv.v_scale[it.kh] : 1.f;
   store_cols128(a.out, it.row0 + tok, (it.kh * a.group + rr - q * a.group) * D, heads * D, lane,
-                make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                make_float4(v.x * f * vs, v.y * f * vs, v.z * f * vs, v.w * f * vs));
 }
 
 template <int D, bool FP8>

@@ -1,5 +1,5 @@
-"""More cases of the paged-attention operators: batches with rows that see nothing, and queries
-at the ends of their range."""
+"""More cases of the paged-attention operators: batches with rows that see nothing, queries
+at the ends of their range, and weights far below the largest."""
 import numpy as np
 import pytest
 
@@ -210,3 +210,93 @@ def test_decode_infinite_queries(pa, D, n):
     p.q[:, :, 4] = -3e38
     got = run(pa, p, p.tensors(), True).double().cpu().numpy()
     assert (got[0] == 0).all() and np.isnan(got[1]).all()
+
+
+# ------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [0, 1, 1000])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first", [True, False])
+def test_many_small_weights_below_a_large_one(pa, D, rows, first, fp8):
+    """One token stands out by 2^25.5 and its value is 0, those of the other 131071 are 1: together they make 0.3 % of a row.
+    rows 0: decode; 1: a prompt in parts; 1000: whole.  A weight is off by 2^-11 of it in fp16 and 2^-8 in bf16, and in fp16
+    by half a step of its smallest, 2^-25, where weights are scaled by 2^7 or more: 2^-32 of the largest for each token.  The sums' chains, of
+    2^13 steps at most, are off by 2^-23 a step; the exponent by three roundings of up to 25.5; the result by 2^-8."""
+    import torch
+    page, n = 128, 1 << 17
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    k, v = torch.zeros(2, 2, 1, page, D, device="cuda")
+    at = 5 if first else page - 7
+    k[1, 0, at, 0] = 1.0
+    v += 1.0
+    v[1, 0, at] = 0.0
+    k, v = k.to(dt), v.to(dt)
+    scale = {x: torch.ones(1, device="cuda") for x in ("k_scale", "v_scale")} if fp8 else {}
+    hq, T = 4, max(rows, 1)
+    cols = n // page + 2
+    table = torch.zeros((1, cols), dtype=torch.int32, device="cuda")
+    table[0, 0 if first else n // page - 1] = 1
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    q = torch.zeros(T, hq, D, device="cuda").bfloat16()
+    q[:, :, 0] = 1.0
+    s = 25.5 * np.log(2.0)
+    if rows:
+        got = pa.prompt_attention(q, k, v, starts, lens, table, scale=s, **scale)
+    else:
+        got = pa.decode_attention(q, k, v, lens, table, scale=s, **scale)
+    got = got.double().cpu().numpy()
+    # (a row that the token which stands out comes after sees even ones only)
+    p = n - T + np.arange(T)
+    seen = p >= (at if first else n - page + at)
+    others = p + 1 - seen
+    small = 2.0 ** -25.5 * others
+    want = np.where(seen, small / (1 + small), 1.0)[:, None, None]
+    lost = others * 2.0 ** -32 * fp8
+    tol = want * (2.0 ** -8 + (2.0 ** -11 if fp8 else 2.0 ** -8) + 2.0 ** -10 + 3 * 25.5 * 2.0 ** -24) + (lost * seen)[:, None, None]
+    assert (np.abs(got - want) <= tol).all(), (got[:, 0, 0], want[:, 0, 0])
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("v_size", [1e-33, 1e30])
+def test_scales_of_values_far_from_one(pa, decode, v_size):
+    """E4M3 caches, the scale of V near the ends of fp32: the sums' own scale does not meet it in one number."""
+    p = Problem([3000, 90], rows=[1, 1] if decode else [70, 90], hq=8, hkv=2, D=64, page=16, fp8=True, seed=53)
+    p.vs = (p.vs * v_size).astype(np.float32)
+    p.v = E4M3_TABLE[p.vc] * p.vs.astype(np.float64)[:, None, None]
+    want, bound = p.expected()
+    check(run(pa, p, p.tensors(), decode).double().cpu().numpy(), want, bound)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,n,rows", [(1, 700, 1), (300, 90, 1), (3, 9000, 1), (3, 9000, 20), (1, 700, 500)])
+def test_small_weights_beside_large_ones_everywhere(pa, B, n, rows, D, fp8):
+    """In each 16 tokens one stands out by 2^25.5 and has no value, the others have all: what they give is small, and
+    known as well as above (decode: half a step of 2^-24 of weights scaled by 2^15, 2^-40)."""
+    import torch
+    page = 32
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    k, v = torch.zeros(2, 1, 1, page, D, device="cuda")
+    k[:, :, ::16, 0] = 1.0
+    v += 1.0
+    v[:, :, ::16] = 0.0
+    k, v = k.to(dt), v.to(dt)
+    scale = {x: torch.ones(1, device="cuda") for x in ("k_scale", "v_scale")} if fp8 else {}
+    table = torch.zeros((B, -(-n // page)), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda") * rows
+    q = torch.zeros(B * rows, 4, D, device="cuda").bfloat16()
+    q[:, :, 0] = 1.0
+    s = 25.5 * np.log(2.0)
+    if rows > 1:
+        got = pa.prompt_attention(q, k, v, starts, lens, table, scale=s, **scale)
+    else:
+        got = pa.decode_attention(q, k, v, lens, table, scale=s, **scale)
+    seen = n - rows + 1 + np.arange(rows)
+    large = (seen + 15) // 16
+    want = (seen - large) * 2.0 ** -25.5 / (large + (seen - large) * 2.0 ** -25.5)
+    lost = (seen - large) / large * (2.0 ** -32 if rows > 1 else 2.0 ** -40) * fp8
+    tol = want * (2.0 ** -8 + (2.0 ** -11 if fp8 else 2.0 ** -8) + 2.0 ** -10 + 3 * 25.5 * 2.0 ** -24) + lost
+    got = got.double().cpu().numpy().reshape(B, rows, -1)
+    assert (np.abs(got - want[:, None]) <= tol[:, None]).all(), (got[0, :, 0], want)
