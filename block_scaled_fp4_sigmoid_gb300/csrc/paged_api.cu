@@ -50,9 +50,10 @@ fp4moe_status check_attn(const fp4moe_kv_cache& c, const fp4moe_attn& a, PagedAt
   if (!a.q || (a.out ? a.codes || a.code_scales : !a.codes || !a.code_scales)) return FP4MOE_ERR_INVALID_ARG;
   if (a.q_heads < 1 || a.q_heads % c.kv_heads != 0 || a.q_heads / c.kv_heads > kMaxGroup) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
   const int group = a.q_heads / c.kv_heads;
+  const float scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   if (a.codes && group * c.head_dim % 128 != 0) return FP4MOE_ERR_UNSUPPORTED_SHAPE;
   if (a.q_ld < (int64_t)a.q_heads * c.head_dim || a.q_ld % 8 != 0 || a.q_ld >= (int64_t)1 << 38 || a.window < 0 || a.sinks < 0 ||
-      !std::isfinite(a.scale) || a.scale < 0)
+      !std::isfinite(scale_log2) || a.scale < 0)
     return FP4MOE_ERR_INVALID_ARG;
   if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.codes, 16) || !aligned(a.code_scales, 4))
     return FP4MOE_ERR_INVALID_ARG;
@@ -63,7 +64,7 @@ fp4moe_status check_attn(const fp4moe_kv_cache& c, const fp4moe_attn& a, PagedAt
   out->group = group;
   out->window = a.window;
   out->sinks = a.sinks;
-  out->scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  out->scale_log2 = scale_log2;
   return FP4MOE_OK;
 }
 

@@ -613,7 +613,7 @@ fp4moe_status fp4moe_kv_append(const fp4moe_kv_cache *cache, const fp4moe_kv_bat
  * Either out bf16 [rows, q_heads * head_dim], or codes (same shape) and
  * code_scales [rows, ceil(q_heads * head_dim / 128)], the E4M3 codes of the block-scaled
  * operators above: then q_heads / kv_heads * head_dim is a multiple of 128.
- * window >= 0 (0: none), sinks >= 0; scale finite and >= 0. */
+ * window >= 0 (0: none), sinks >= 0; scale >= 0, and scale * log2(e) finite in fp32. */
 typedef struct {
   const uint16_t *q;
   int64_t q_ld;

@@ -332,3 +332,10 @@ def test_workspace_holds_what_a_call_of_any_size_leaves(pa):
         assert fm.attn_decode_workspace_size(c, 8) >= 2 * 152 * 2 * 16 * (4 * D + 8)
         assert fm.attn_prompt_workspace_size(c, 8) >= 152 * 256 * (4 * D + 8)
     assert np.int64(fm.attn_decode_workspace_size(cache(), 128)) > 0
+
+
+@pytest.mark.parametrize("call", [decode, prompt])
+def test_scales_whose_softmax_in_base_2_has_none(pa, call):
+    """scale * log2(e) is fp32: infinite from 2.36e38 on, where a score of 0 would be NaN."""
+    assert call(a=dict(scale=2.3e38)) == 0
+    assert call(a=dict(scale=2.4e38)) == INVALID
