@@ -300,3 +300,133 @@ def test_small_weights_beside_large_ones_everywhere(pa, B, n, rows, D, fp8):
     tol = want * (2.0 ** -8 + (2.0 ** -11 if fp8 else 2.0 ** -8) + 2.0 ** -10 + 3 * 25.5 * 2.0 ** -24) + lost
     got = got.double().cpu().numpy().reshape(B, rows, -1)
     assert (np.abs(got - want[:, None]) <= tol[:, None]).all(), (got[0, :, 0], want)
+
+
+# ------------------------------------------------------------- calls that the header allows
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prompts_in_a_captured_graph_follow_their_tensors(pa, fp8):
+    """Prompts of a padded batch, captured once and replayed as sequences and rows change (a sequence that was padding
+    gets tokens, another one ends), over one workspace in two graphs."""
+    import torch
+    rng = np.random.default_rng(70)
+    ps = []
+    for lens, rows in (([900, 0, 700, 0], [30, 1, 60, 9]), ([0, 300, 2500, 5], [1, 90, 8, 1]), ([0, 0, 0, 0], [25, 25, 25, 25])):
+        p = Problem(lens, rows=rows, hq=16, hkv=4, D=64, page=32, fp8=fp8, seed=71)
+        p.q = p.q[:100]
+        ps.append(p)
+    k, v = (torch.zeros((200, 4, 32, 64), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda") for _ in range(2))
+    q, out = (torch.zeros((100, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lens, starts, table = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((4,), (5,), (4, 90)))
+    ks, vs = (torch.ones(4, device="cuda") for _ in range(2)) if fp8 else (None, None)
+    ws = torch.empty(pa.prompt_workspace_size(k, 16), dtype=torch.uint8, device="cuda")
+
+    def call():
+        pa.prompt_attention(q, k, v, starts, lens, table, k_scale=ks, v_scale=vs, ws=ws, out=out)
+
+    call()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for i in range(6):
+        p = ps[i % 3]
+        t = p.tensors()
+        n = len(p.q)
+        q[:n] = t["q"]
+        k[:p.pages], v[:p.pages] = t["k_cache"], t["v_cache"]
+        table.fill_(-1)
+        table[:, :p.table.shape[1]] = t["table"]
+        lens.copy_(t["lens"])
+        starts.copy_(t["starts"])
+        if fp8:
+            ks.copy_(t["k_scale"])
+            vs.copy_(t["v_scale"])
+        out.fill_(7)
+        graphs[i % 2].replay()
+        want, bound = p.expected()
+        got = out.double().cpu().numpy()
+        check(got[:n], want, bound)
+        assert (got[n:] == 7).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (1, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (0, 2 ** 31 - 1)])
+def test_the_largest_windows_and_sinks(pa, window, sinks, decode, fp8):
+    rows = [1, 1, 1] if decode else [70, 3, 130]
+    holds(pa, Problem([300, 3, 2000], rows=rows, hq=8, hkv=2, D=128, page=32, fp8=fp8, window=window, sinks=sinks, seed=72), decode)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("value", [2 ** 31 - 1, -2 ** 31])
+def test_lengths_that_are_no_lengths(pa, value, fp8):
+    """Lengths past the table and below zero: zeros, nothing is stored, and the other sequences are what they are."""
+    import torch
+    p = Problem([300, 40, 130], rows=[1, 1, 1], hq=8, hkv=2, D=64, page=16, fp8=fp8, seed=73)
+    t = p.tensors()
+    q = t["q"]
+    for prompt in (False, True):
+        want = run(pa, p, t, not prompt)
+        lens = t["lens"].clone()
+        lens[1] = value
+        got = run(pa, p, {**t, "lens": lens}, not prompt)
+        assert not got[1].any() and torch.equal(got[[0, 2]], want[[0, 2]])
+    new = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    rope = torch.ones(p.table.shape[1] * p.page, 64, device="cuda")
+    k, v = t["k_cache"].clone(), t["v_cache"].clone()
+    one, three = torch.full_like(q, 7), torch.full_like(q, 7)
+    more = {"k_scale": t["k_scale"], "v_scale": t["v_scale"]}
+    pa.append_kv(q, new, new, rope, k, v, lens, t["table"], q_out=one, **more)
+    assert not one[1].any()
+    lens[1] = 0
+    pa.append_kv(q, new, new, rope, t["k_cache"], t["v_cache"], lens, t["table"], q_out=three, **more)
+    assert torch.equal(one, three)
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    assert same(k, t["k_cache"]) and same(v, t["v_cache"])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_rows_in_front_of_the_first_sequence(pa, D, fp8):
+    """starts that begin behind row 0, queries that are ranges of wider rows."""
+    import torch
+    p = Problem([200, 0, 90], rows=[70, 3, 90], hq=8, hkv=2, D=D, page=16, fp8=fp8, seed=74)
+    t = p.tensors()
+    want = run(pa, p, t)
+    wide = torch.full((p.T + 9, 12, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[5:5 + p.T, 2:10] = t["q"]
+    out = torch.full((p.T + 9, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    run(pa, p, {**t, "q": wide[:, 2:10], "starts": t["starts"] + 5}, out=out)
+    assert torch.equal(out[5:5 + p.T], want) and (out[:5] == 7).all() and (out[5 + p.T:] == 7).all()
+
+
+@pytest.mark.parametrize("R", [0, 64])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sublayer_of_a_padded_batch(pa, R, fp8):
+    """Padding rows, which hold NaN, leave the other rows what they are, and are what the output product makes of zeros."""
+    import torch
+    torch.manual_seed(75)
+    H, hq, hkv, D, page, B = 512, 16, 4, 64, 16, 30
+    w = lambda m, n: (torch.randint(0, 120, (m, n), device="cuda").to(torch.uint8), torch.rand(-(-m // 128), -(-n // 128), device="cuda") * 1e-3)  # noqa: E731
+    gamma = torch.ones(H, device="cuda").bfloat16()
+    a = torch.rand(12 * page, R // 2, device="cuda")
+    scales = {"k_scale": torch.full((hkv,), 0.1, device="cuda"), "v_scale": torch.full((hkv,), 0.1, device="cuda")} if fp8 else {}
+    layer = pa.Fp8BlockAttention(gamma, *w((hq + 2 * hkv) * D, H), *w(H, hq * D), hq, hkv, D,
+                                 torch.cat((a.cos(), a.sin()), 1) if R else None, **scales)
+    table = torch.randperm(B * 12, device="cuda").view(B, 12).int()
+    rows = [100 + i for i in range(15)] + [1 + i % 3 for i in range(15)]
+    lens = torch.tensor([n if i < 15 else 0 for i, n in enumerate(rows)], dtype=torch.int32, device="cuda")
+    starts = torch.tensor(np.cumsum([0] + rows), dtype=torch.int32, device="cuda")
+    n, T = int(starts[15]), int(starts[-1])
+    x, r = (torch.randn(T, H, device="cuda").bfloat16() for _ in range(2))
+    x[n:] = float("nan")
+    new = lambda: torch.zeros(B * 12, hkv, page, D, device="cuda").to(torch.float8_e4m3fn if fp8 else torch.bfloat16)  # noqa: E731
+    (k, v), (k2, v2) = (new(), new()), (new(), new())
+    want, _ = layer.forward(x[:n], r[:n], k, v, lens[:15], table[:15], starts[:16])
+    for _ in range(5):
+        got, _ = layer.forward(x, r, k2, v2, lens, table, starts)
+        assert torch.equal(got[:n], want) and not got[n:].any()
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    assert same(k, k2) and same(v, v2)
