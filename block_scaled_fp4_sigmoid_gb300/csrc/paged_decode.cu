@@ -14,6 +14,9 @@
 // and operands come straight from the ring), the queries that share a key-value
 // head, 8 or 16, their columns; running maximum and sum of the softmax stay in
 // registers and the warps' sums are joined in shared memory when the head changes.
+// Weights are rounded to the operands' type, bf16 (2^-8 of each, as a bf16 output is rounded by 2^-8, and over many
+// tokens less) or, for E4M3 caches, fp16 (f16x2_weights; q too, below); the sums have them unrounded.  The exponentials are
+// ex2.approx, off by 2^-22 or so of themselves.
 // (With the queries as the 16 rows, a group of 4 or 8 took twice the products, twice the
 // exponentials and twice the registers: 64 sequences of up to 16000, E4M3, 177 us, now 168.)
 #include "paged.h"

@@ -15,16 +15,21 @@
 //
 // What bounds it: heads of 128, a tile's own chain: 1400 cycles of softmax and 1024 of MMAs and the
 // waits between, where the two tiles' MMAs alone would take 2048 (8192 rows of 32 heads: 311 us,
-// 1770 TFLOP/s).  So P goes to P V in three parts, the first while the rest is computed (whole
-// halves: 326 us).  Tensor memory is full then: 2 S and 2 O of 128 columns.  Heads of 64 have room for
-// a third S, and the softmax is the bound (24 heads, window of 1024, 3 sequences of up to 6001: 130 us,
-// with two 142).  16 softmax warps, half a row a thread, were slower (371 us): the halves of a
-// row have to tell each other their maximum.
+// 1770 TFLOP/s, replayed from a graph a dozen times; 340 to 350 us in long runs of calls, where the power
+// cap lowers the clock; the other times here are of graphs too).  So P goes to P V in three parts, the first while the rest is
+// computed (whole halves: 326 us).  Tensor memory is full then: 2 S and 2 O of 128 columns.  Heads of 64
+// have room for a third S (24 heads, window of 1024, 3 sequences of up to 6001: 130 us, with two 142).  There no
+// pipe is full (tensor cores and exponentials a third, issue half): eight warps' chains of wait, fetch, maximum,
+// exponentials and store bound it, and the starts and ends of pieces of some ten tiles.  16 softmax warps, half a
+// row a thread, were slower (371 us): the halves of a row have to tell each other their maximum.
+//
+// P is rounded to bf16, an operand's type, for P V (the row's sum has it unrounded): 2^-8 of each weight, as
+// a bf16 output is rounded by 2^-8, and over many tokens less.  The exponentials are ex2.approx, off by 2^-22 or so of themselves.
 //
 // E4M3 caches: K goes into the products as it is, with Q as the sum of two E4M3 numbers
-// (a bf16 value is one, to 2^-18 of its row's largest).  P would not be: its small values
+// (a bf16 value is one, to 2^-17 of its row's largest).  P would not be: its small values
 // matter together.  So four more warps turn each tile of V into fp16, exactly, and P is
-// fp16.  (1024 rows behind 24000 tokens, twice, 32 heads: 550 us; with K converted
+// fp16, scaled by 2^7 (f16x2_weights).  (1024 rows behind 24000 tokens, twice, 32 heads: 543 to 549 us; with K converted
 // too 711: shared memory, which the conversion reads and writes as well, had 2500 cycles of work a tile.)
 //
 // What a row may not see is masked in S; in P V its values count 0 times.  Infinities and NaN
@@ -811,8 +816,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FP8>::kThreads, 1) prompt_kernel(
       if constexpr (FP8) {
         // Q as the sum of two E4M3 numbers, for products with the cache's codes as they are.
         // Scaled by the power of two that brings a row's largest magnitude to 128 .. 256, the 8 bits
-        // of a bf16 value are the first number's 4 and a remainder of 4: exact down to 2^-10 of
-        // the largest, and off by 2^-18 of it at most below.
+        // of a bf16 value are the first number's 4 and a remainder of 4: exact down to 2^-9 of
+        // the largest, and below off by half of E4M3's smallest step, 2^-10: 2^-17 of the largest at most.
+        // (A largest one below 2^-119 comes to less than 128.)
         if (!(ok = wait_w(&bar_q, queries & 1))) break;
         if (t < w.tiles) {
           uint4 q[D / 8];

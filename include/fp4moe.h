@@ -605,11 +605,13 @@ fp4moe_status fp4moe_kv_append(const fp4moe_kv_cache *cache, const fp4moe_kv_bat
  * j <= p that are cached, not in a hole, and (window > 0) have p - j < window or j < sinks:
  *   out = sum_j softmax_j(scale * q . k_j) v_j,  zeros where nothing is seen or all
  * scores are -infinity.  Scores, softmax sums and outputs are held in fp32; the softmax weights
- * are rounded to bf16 (fp8 cache: fp16) for their product with v.  With an fp8 cache q is
- * rounded too, a head's row scaled by a power of two: to fp16 (decode) or to the sum of two E4M3
- * numbers (prompt), off by 2^-18 of the row's largest magnitude at most.  What a token holds
+ * are rounded to bf16 (fp8 cache: fp16, in which those above 2^-32 of the largest count) for their
+ * product with v.  With an fp8 cache q is rounded too, a head's row scaled by a power of two: to fp16
+ * (decode) or to the sum of two E4M3 numbers (prompt), off by 2^-17 of the row's largest magnitude at
+ * most (where that is 2^-119 or more).  What a token holds
  * does not reach a row that does not see it, infinities and NaN included.  (Prompts: a row among
- * whose tile's values there are such is computed again on its own, which takes longer.)
+ * whose tile's values there are such, or with an fp8 cache one whose q holds an infinity, is computed
+ * again on its own, which takes longer.)
  * Either out bf16 [rows, q_heads * head_dim], or codes (same shape) and
  * code_scales [rows, ceil(q_heads * head_dim / 128)], the E4M3 codes of the block-scaled
  * operators above: then q_heads / kv_heads * head_dim is a multiple of 128.
